@@ -456,3 +456,11 @@ def moe_grouped_gemm_wgrad(b, a, counts, offsets, c, bind=False):
     return _run("moe_grouped_gemm_wgrad", bind, (
         _ptr(b, "b"), _ptr(a, "a"), dtype_code(b), _i32(counts, "counts"), _i32(offsets, "offsets"),
         L, rows_cap, N, K, _f32(c, "c"), _stream(b)))
+
+
+# ---------------------------------------------------------------- the block around the share (libmoe_block.so)
+
+from . import block as _block  # noqa: E402  (after the helpers that it uses)
+from .block import *  # noqa: E402,F401,F403
+
+__all__ += _block.__all__

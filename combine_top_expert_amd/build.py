@@ -1,12 +1,13 @@
-"""Build libmoe_ep.so (gfx950) in-tree with hipcc.
+"""Build libmoe_ep.so and libmoe_block.so (gfx950) in-tree with hipcc.
 
     python combine_top_expert_amd/build.py [--jobs N]
 
 (Run it as a script, not as ``-m combine_top_expert_amd.build``: importing the
 package loads the library, which may be missing or stale before a build.)
 
-Compiles every source under csrc/ to an object in _build/ (in parallel) and
-links them into combine_top_expert_amd/libmoe_ep.so.  Always rebuilds.
+Compiles every source under csrc/ and csrc/block/ to an object in _build/ (in
+parallel) and links the two folders' objects into
+combine_top_expert_amd/libmoe_ep.so and libmoe_block.so.  Always rebuilds.
 """
 from __future__ import annotations
 
@@ -23,6 +24,7 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 BUILD = PKG / "_build"
 LIB = PKG / "libmoe_ep.so"
+LIB_BLOCK = PKG / "libmoe_block.so"
 ARCH = os.environ.get("MOE_OFFLOAD_ARCH", "gfx950")
 
 # Packed fp32 (v_pk_*_f32) is turned off for all device code.
@@ -42,7 +44,7 @@ def hipcc() -> str:
 
 
 def _compile(src: Path) -> Path:
-    obj = BUILD / (src.stem + src.suffix.replace(".", "_") + ".o")
+    obj = BUILD / ("_".join(src.relative_to(CSRC).parts).replace(".", "_") + ".o")
     cmd = [hipcc(), *HIPCC_FLAGS, "-c", str(src), "-o", str(obj)]
     if src.suffix == ".cpp":
         cmd.insert(1, "-x")
@@ -56,12 +58,8 @@ def _compile(src: Path) -> Path:
     return obj
 
 
-def build(jobs: int = 8, verbose: bool = True) -> Path:
-    BUILD.mkdir(exist_ok=True)
-    srcs = sorted(list(CSRC.glob("*.hip")) + list(CSRC.glob("*.cpp")))
-    with ThreadPoolExecutor(max_workers=max(1, min(jobs, len(srcs)))) as ex:
-        objs = list(ex.map(_compile, srcs))
-    tmp = LIB.with_suffix(".so.tmp")
+def _link(objs, lib: Path) -> None:
+    tmp = lib.with_suffix(".so.tmp")
     # --no-undefined: an unresolved symbol (e.g. a kernel stub the host pass
     # did not emit) fails the build instead of the first dlopen
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,--no-undefined", "-o", str(tmp),
@@ -69,9 +67,20 @@ def build(jobs: int = 8, verbose: bool = True) -> Path:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    if verbose:
-        print(f"built {LIB} from {len(srcs)} sources")
+    os.replace(tmp, lib)
+
+
+def build(jobs: int = 8, verbose: bool = True) -> Path:
+    BUILD.mkdir(exist_ok=True)
+    groups = {lib: sorted(list(d.glob("*.hip")) + list(d.glob("*.cpp")))
+              for lib, d in ((LIB, CSRC), (LIB_BLOCK, CSRC / "block"))}
+    srcs = [src for g in groups.values() for src in g]
+    with ThreadPoolExecutor(max_workers=max(1, min(jobs, len(srcs)))) as ex:
+        objs = dict(zip(srcs, ex.map(_compile, srcs)))
+    for lib, g in groups.items():
+        _link([objs[src] for src in g], lib)
+        if verbose:
+            print(f"built {lib} from {len(g)} sources")
     return LIB
 
 
