@@ -15,7 +15,7 @@ from pathlib import Path
 
 import torch
 
-from . import MOE_EPI_SILU_MUL, MOE_EPI_STORE_G, MOE_FP8_E4M3, MoEError, _f32, _i32, _need, _offsets, _ptr, _shape, _stream, dtype_code
+from . import MOE_BF16, MOE_EPI_SILU_MUL, MOE_EPI_STORE_G, MOE_F32, MOE_FP8_E4M3, MoEError, _need, _offsets, _stream
 
 __all__ = [
     "BLOCK_LIB_PATH", "block_lib", "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_W4_INT4", "MOE_W4_E2M1",
@@ -59,46 +59,76 @@ def moe_block_abi_version() -> int:
 
 
 # ---------------------------------------------------------------- marshalling helpers
+#
+# A decode step calls these operators for a few microseconds of GPU time each,
+# so a call's checks are one pass over its tensors that only compares, and what
+# is wrong is found out where something is.
 
-def _one_device(ref: torch.Tensor, **others: torch.Tensor | None) -> None:
-    for name, t in others.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
-
-
-def _like(ref: torch.Tensor, **others: torch.Tensor | None) -> None:
-    """Raise unless every given tensor has ref's dtype."""
-    for name, t in others.items():
-        if t is not None and t.dtype != ref.dtype:
-            raise TypeError(f"{name} has dtype {t.dtype}, expected {ref.dtype}")
+_CODE = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float8_e4m3fn: MOE_FP8_E4M3,
+         torch.uint8: MOE_FP8_E4M3}
+_F32, _I32, _U8 = (torch.float32,), (torch.int32,), (torch.uint8,)
+_REAL, _FP8 = (torch.float32, torch.bfloat16), (torch.float8_e4m3fn, torch.uint8)
+_ANY = tuple(_CODE)
 
 
-def _fp8(t: torch.Tensor | None, name: str) -> int | None:
-    if t is not None and dtype_code(t) != MOE_FP8_E4M3:
-        raise TypeError(f"{name} must hold e4m3fn codes (float8_e4m3fn or uint8)")
-    return _ptr(t, name)
+def _refuse(specs) -> None:
+    """Raise for the first fault among (name, tensor, dtypes, shape): shapes
+    and dtypes first (the C ABI receives sizes, not extents), then placement."""
+    given = [s for s in specs if s[1] is not None]
+    for name, t, _, shape in given:
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    for name, t, dtypes, _ in given:
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    for name, t, _, _ in given:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        if t.device != given[0][1].device:
+            raise ValueError(f"{name} is on {t.device}, expected {given[0][1].device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    raise ValueError("unsupported tensor arguments")
 
 
-def _u8(t: torch.Tensor, name: str) -> int | None:
-    if t.dtype != torch.uint8:
-        raise TypeError(f"{name} must be uint8")
-    return _ptr(t, name)
+def _pointers(*specs):
+    """Device index of the first tensor and the data pointers of all (None for
+    None), each checked for device, dtype, shape and contiguity."""
+    dev = specs[0][1].get_device()
+    out = []
+    for _, t, dtypes, shape in specs:
+        if t is None:
+            out.append(None)
+            continue
+        if dev < 0 or t.get_device() != dev or t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+            _refuse(specs)
+        out.append(t.data_ptr())
+    return dev, out
 
 
-def _run(fn: str, bind: bool, ref: torch.Tensor, args: tuple):
-    """Call C entry point ``fn`` with ref's device current (launches go to the
+# the current stream's handle without building a torch.cuda.Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: _stream(torch.empty(0, device=torch.device("cuda", dev))))
+
+
+def _run(fn: str, bind: bool, dev: int, args: tuple):
+    """Call C entry point ``fn`` with device ``dev`` current (launches go to the
     current device), or return that call as a zero-argument callable."""
-    f, dev = getattr(block_lib, fn), ref.device.index
+    f = getattr(block_lib, fn)
 
-    def call():
-        if torch.cuda.current_device() == dev:
+    if bind:
+        return lambda: _run_now(fn, f, dev, args)
+    return _run_now(fn, f, dev, args)
+
+
+def _run_now(fn, f, dev, args):
+    if torch.cuda.current_device() == dev:
+        st = f(*args)
+    else:
+        with torch.cuda.device(dev):
             st = f(*args)
-        else:
-            with torch.cuda.device(dev):
-                st = f(*args)
-        if st != 0:
-            raise MoEError(fn, st)
-    return call if bind else call()
+    if st != 0:
+        raise MoEError(fn, st)
 
 
 # ---------------------------------------------------------------- norm
@@ -107,20 +137,17 @@ def moe_add_rms_norm(x, residual, weight, eps, h_out=None, y=None, y8=None, y8_s
     """x [T,H] (+ residual [T,H], or None) -> h_out = x + residual, y = its RMS
     norm times weight [H], y8/y8_scales = y in block FP8 (any of the three may
     be None).  h_out or y may be x or residual itself."""
-    T, H = x.shape
-    _shape(residual, "residual", T, H)
-    _shape(weight, "weight", H)
-    _shape(h_out, "h_out", T, H)
-    _shape(y, "y", T, H)
-    _shape(y8, "y8", T, H)
-    _need(y8_scales, "y8_scales", y8 is not None)
-    _need(y8, "y8", y8_scales is not None)
-    _shape(y8_scales, "y8_scales", T, H // 128)
-    _like(x, residual=residual, h_out=h_out, y=y)
-    _one_device(x, residual=residual, weight=weight, h_out=h_out, y=y, y8=y8, y8_scales=y8_scales)
-    return _run("moe_add_rms_norm", bind, x, (
-        _ptr(x, "x"), _ptr(residual, "residual"), dtype_code(x), _ptr(weight, "weight"), dtype_code(weight), eps, T, H,
-        _ptr(h_out, "h_out"), _ptr(y, "y"), _fp8(y8, "y8"), _f32(y8_scales, "y8_scales"), _stream(x)))
+    T, H = rows = x.shape
+    dt = (x.dtype,) if x.dtype in _REAL else _REAL
+    if y8 is not None or y8_scales is not None:
+        _need(y8_scales, "y8_scales", True)
+        _need(y8, "y8", True)
+    dev, (px, pr, pw, ph, py, p8, ps) = _pointers(
+        ("x", x, dt, rows), ("residual", residual, dt, rows), ("weight", weight, _REAL, (H,)),
+        ("h_out", h_out, dt, rows), ("y", y, dt, rows), ("y8", y8, _FP8, rows),
+        ("y8_scales", y8_scales, _F32, (T, H // 128)))
+    return _run("moe_add_rms_norm", bind, dev, (
+        px, pr, _CODE[x.dtype], pw, _CODE[weight.dtype], eps, T, H, ph, py, p8, ps, _raw_stream(dev)))
 
 
 def moe_add_rms_norm_backward_workspace_bytes(T: int, H: int) -> int:
@@ -129,19 +156,17 @@ def moe_add_rms_norm_backward_workspace_bytes(T: int, H: int) -> int:
 
 def moe_add_rms_norm_backward(dy, h, weight, eps, dx, d_weight, workspace, dh=None, bind=False):
     """dy [T,H], the forward's h [T,H] (and dh [T,H], the gradient of h_out) ->
-    dx [T,H], the gradient of x and of residual, and d_weight [H] fp32."""
-    T, H = dy.shape
-    _shape(h, "h", T, H)
-    _shape(dh, "dh", T, H)
-    _shape(dx, "dx", T, H)
-    _shape(weight, "weight", H)
-    _shape(d_weight, "d_weight", H)
-    _like(dy, h=h, dh=dh, dx=dx)
-    _one_device(dy, h=h, dh=dh, dx=dx, weight=weight, d_weight=d_weight, workspace=workspace)
-    return _run("moe_add_rms_norm_backward", bind, dy, (
-        _ptr(dy, "dy"), _ptr(h, "h"), _ptr(dh, "dh"), dtype_code(dy), _ptr(weight, "weight"), dtype_code(weight), eps,
-        T, H, _ptr(dx, "dx"), _f32(d_weight, "d_weight"), _ptr(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(dy)))
+    dx [T,H], the gradient of x and of residual, and d_weight [H] fp32.
+    workspace: moe_add_rms_norm_backward_workspace_bytes(T, H) bytes or more."""
+    T, H = rows = dy.shape
+    dt = (dy.dtype,) if dy.dtype in _REAL else _REAL
+    dev, (pdy, ph, pdh, pw, pdx, pdw, pws) = _pointers(
+        ("dy", dy, dt, rows), ("h", h, dt, rows), ("dh", dh, dt, rows), ("weight", weight, _REAL, (H,)),
+        ("dx", dx, dt, rows), ("d_weight", d_weight, _F32, (H,)),
+        ("workspace", workspace, (workspace.dtype,), workspace.shape))
+    return _run("moe_add_rms_norm_backward", bind, dev, (
+        pdy, ph, pdh, _CODE[dy.dtype], pw, _CODE[weight.dtype], eps, T, H, pdx, pdw, pws,
+        workspace.numel() * workspace.element_size(), _raw_stream(dev)))
 
 
 # ---------------------------------------------------------------- routing
@@ -150,30 +175,26 @@ def moe_router_group_topk(logits, K, topk_ids, topk_weights, bias=None, score=MO
                           topk_group=1, group_top=2, renorm=True, route_scale=1.0, bind=False):
     """logits [T,E] fp32 (+ bias [E] fp32, for the choice only) -> topk_ids
     [T,K] int32 (-1 where no expert remains), topk_weights [T,K] fp32."""
-    T, E = logits.shape
-    _shape(bias, "bias", E)
-    _shape(topk_ids, "topk_ids", T, K)
-    _shape(topk_weights, "topk_weights", T, K)
-    _one_device(logits, bias=bias, topk_ids=topk_ids, topk_weights=topk_weights)
-    return _run("moe_router_group_topk", bind, logits, (
-        _f32(logits, "logits"), _f32(bias, "bias"), T, E, K, int(score), n_group, topk_group, group_top,
-        1 if renorm else 0, route_scale, _i32(topk_ids, "topk_ids"), _f32(topk_weights, "topk_weights"),
-        _stream(logits)))
+    T, E = rows = logits.shape
+    dev, (pl, pb, pi, pw) = _pointers(
+        ("logits", logits, _F32, rows), ("bias", bias, _F32, (E,)), ("topk_ids", topk_ids, _I32, (T, K)),
+        ("topk_weights", topk_weights, _F32, (T, K)))
+    return _run("moe_router_group_topk", bind, dev, (
+        pl, pb, T, E, K, score, n_group, topk_group, group_top, 1 if renorm else 0, route_scale, pi, pw,
+        _raw_stream(dev)))
 
 
 def moe_router_group_topk_backward(logits, topk_ids, d_weights, d_logits, score=MOE_SCORE_SIGMOID, renorm=True,
                                    route_scale=1.0, bind=False):
     """d_weights [T,K] (gradient of topk_weights), the forward's logits [T,E]
     and topk_ids [T,K] -> d_logits [T,E] fp32, every element written."""
-    T, E = logits.shape
+    T, E = rows = logits.shape
     K = topk_ids.shape[1]
-    _shape(topk_ids, "topk_ids", T, K)
-    _shape(d_weights, "d_weights", T, K)
-    _shape(d_logits, "d_logits", T, E)
-    _one_device(logits, topk_ids=topk_ids, d_weights=d_weights, d_logits=d_logits)
-    return _run("moe_router_group_topk_backward", bind, logits, (
-        _f32(logits, "logits"), _i32(topk_ids, "topk_ids"), _f32(d_weights, "d_weights"), T, E, K, int(score),
-        1 if renorm else 0, route_scale, _f32(d_logits, "d_logits"), _stream(logits)))
+    dev, (pl, pi, pdw, pdl) = _pointers(
+        ("logits", logits, _F32, rows), ("topk_ids", topk_ids, _I32, (T, K)),
+        ("d_weights", d_weights, _F32, (T, K)), ("d_logits", d_logits, _F32, rows))
+    return _run("moe_router_group_topk_backward", bind, dev, (
+        pl, pi, pdw, T, E, K, score, 1 if renorm else 0, route_scale, pdl, _raw_stream(dev)))
 
 
 # ---------------------------------------------------------------- dispatch of FP8 rows
@@ -182,15 +203,11 @@ def moe_permute_fp8(x8, x8_scales, slot_of, buf, buf_scales, bind=False):
     """x8 [T,H] e4m3fn with x8_scales [T,H/128], slot_of [T,K] -> buf
     [rows_cap,H], buf_scales [rows_cap,H/128], copied bit for bit."""
     T, H = x8.shape
-    K = slot_of.shape[1]
-    _shape(x8_scales, "x8_scales", T, H // 128)
-    _shape(slot_of, "slot_of", T, K)
-    _shape(buf, "buf", buf.shape[0], H)
-    _shape(buf_scales, "buf_scales", buf.shape[0], H // 128)
-    _one_device(x8, x8_scales=x8_scales, slot_of=slot_of, buf=buf, buf_scales=buf_scales)
-    return _run("moe_permute_fp8", bind, x8, (
-        _fp8(x8, "x8"), _f32(x8_scales, "x8_scales"), T, K, H, _i32(slot_of, "slot_of"), buf.shape[0],
-        _fp8(buf, "buf"), _f32(buf_scales, "buf_scales"), _stream(x8)))
+    K, cap = slot_of.shape[1], buf.shape[0]
+    dev, (px, pxs, psl, pb, pbs) = _pointers(
+        ("x8", x8, _FP8, (T, H)), ("x8_scales", x8_scales, _F32, (T, H // 128)), ("slot_of", slot_of, _I32, (T, K)),
+        ("buf", buf, _FP8, (cap, H)), ("buf_scales", buf_scales, _F32, (cap, H // 128)))
+    return _run("moe_permute_fp8", bind, dev, (px, pxs, T, K, H, psl, cap, pb, pbs, _raw_stream(dev)))
 
 
 # ---------------------------------------------------------------- 4-bit weights
@@ -207,14 +224,13 @@ def moe_pack_w4(codes, scales, fmt, codes_packed, scales_packed, bind=False):
     moe_grouped_gemv_w4 reads (same shapes and dtypes)."""
     L, N, half = codes.shape
     group = _group(2 * half, scales, "scales")
-    _shape(scales, "scales", L, N, 2 * half // group)
-    _shape(codes_packed, "codes_packed", L, N, half)
-    _shape(scales_packed, "scales_packed", *scales.shape)
-    _like(scales, scales_packed=scales_packed)
-    _one_device(codes, scales=scales, codes_packed=codes_packed, scales_packed=scales_packed)
-    return _run("moe_pack_w4", bind, codes, (
-        _u8(codes, "codes"), _ptr(scales, "scales"), dtype_code(scales), int(fmt), L, N, 2 * half, group,
-        _u8(codes_packed, "codes_packed"), _ptr(scales_packed, "scales_packed"), _stream(codes)))
+    dt = (scales.dtype,) if scales.dtype in _REAL else _REAL
+    per = (L, N, 2 * half // group)
+    dev, (pc, ps, qc, qs) = _pointers(
+        ("codes", codes, _U8, (L, N, half)), ("scales", scales, dt, per),
+        ("codes_packed", codes_packed, _U8, (L, N, half)), ("scales_packed", scales_packed, dt, per))
+    return _run("moe_pack_w4", bind, dev, (
+        pc, ps, _CODE[scales.dtype], fmt, L, N, 2 * half, group, qc, qs, _raw_stream(dev)))
 
 
 def moe_grouped_gemv_w4(a, a_scales, codes_packed, scales_packed, fmt, counts, offsets, epi, out, bind=False):
@@ -223,23 +239,20 @@ def moe_grouped_gemv_w4(a, a_scales, codes_packed, scales_packed, fmt, counts, o
     [rows_cap,N/2] = SiLU(gate) * up (fp32|bf16), on valid rows only."""
     L, N, half = codes_packed.shape
     rows_cap, K = a.shape[0], 2 * half
-    _shape(a, "a", rows_cap, K)
     group = _group(K, scales_packed, "scales_packed")
-    _shape(scales_packed, "scales_packed", L, N, K // group)
-    fp8 = dtype_code(a) == MOE_FP8_E4M3
+    fp8 = a.dtype in _FP8
     _need(a_scales, "a_scales", fp8)
-    if fp8:
-        _shape(a_scales, "a_scales", rows_cap, K // 128)
-    elif a_scales is not None:
+    if not fp8 and a_scales is not None:
         raise ValueError("a_scales goes with FP8 rows only")
-    _shape(counts, "counts", L)
-    _offsets(offsets, L)
-    if int(epi) not in (MOE_EPI_STORE_G, MOE_EPI_SILU_MUL):
+    if epi not in (MOE_EPI_STORE_G, MOE_EPI_SILU_MUL):
         raise ValueError(f"epi is {epi}, expected MOE_EPI_STORE_G or MOE_EPI_SILU_MUL")
-    _shape(out, "out", rows_cap, N if int(epi) == MOE_EPI_STORE_G else N // 2)
-    _one_device(a, a_scales=a_scales, codes_packed=codes_packed, scales_packed=scales_packed, counts=counts,
-                offsets=offsets, out=out)
-    return _run("moe_grouped_gemv_w4", bind, a, (
-        _ptr(a, "a"), dtype_code(a), _f32(a_scales, "a_scales"), _u8(codes_packed, "codes_packed"),
-        _ptr(scales_packed, "scales_packed"), dtype_code(scales_packed), int(fmt), group, _i32(counts, "counts"),
-        _i32(offsets, "offsets"), L, rows_cap, N, K, int(epi), _ptr(out, "out"), dtype_code(out), _stream(a)))
+    _offsets(offsets, L)
+    dev, (pa, pas, pc, ps, pn, po, pout) = _pointers(
+        ("a", a, _ANY, (rows_cap, K)), ("a_scales", a_scales, _F32, (rows_cap, K // 128)),
+        ("codes_packed", codes_packed, _U8, (L, N, half)),
+        ("scales_packed", scales_packed, _REAL, (L, N, K // group)), ("counts", counts, _I32, (L,)),
+        ("offsets", offsets, _I32, offsets.shape),
+        ("out", out, _REAL, (rows_cap, N if epi == MOE_EPI_STORE_G else N // 2)))
+    return _run("moe_grouped_gemv_w4", bind, dev, (
+        pa, _CODE[a.dtype], pas, pc, ps, _CODE[scales_packed.dtype], fmt, group, pn, po, L, rows_cap, N, K, epi, pout,
+        _CODE[out.dtype], _raw_stream(dev)))

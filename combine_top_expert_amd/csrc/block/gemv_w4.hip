@@ -29,9 +29,9 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kWaves = 4;
-constexpr int kThreads = kWaves * MOE_WAVE;
-constexpr int kTiles = 4;                       // 16-row weight tiles of a workgroup
+constexpr int kSimds = 1024;                    // of an MI355X
+constexpr int kMaxWaves = 8;                    // of a workgroup
+constexpr int kTiles = 4;                       // 16-row weight tiles of a wave
 
 // ---------------------------------------------------------------- packing
 
@@ -93,27 +93,28 @@ template <int FMT> __device__ __forceinline__ bf16x8 unpack(uint32_t v) {
   }
 }
 
-// 8 activations of one row: bf16 as they are, e4m3 codes converted exactly
-template <bool FP8> __device__ __forceinline__ bf16x8 load_act(const uint8_t* p) {
-  if constexpr (!FP8) {
-    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(p));
-  } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    return as_bf16x8(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v.x, 1.0f, false)),
-                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v.x, 1.0f, true)),
-                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v.y, 1.0f, false)),
-                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v.y, 1.0f, true)));
-  }
+// 8 activations of one row as loaded, and as the matrix cores take them (e4m3
+// codes convert exactly)
+template <bool FP8> struct Act { uint4 v; };
+template <> struct Act<true> { uint2 v; };
+__device__ __forceinline__ bf16x8 act_bf16(const Act<false>& a) { return __builtin_bit_cast(bf16x8, a.v); }
+__device__ __forceinline__ bf16x8 act_bf16(const Act<true>& a) {
+  return as_bf16x8(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a.v.x, 1.0f, false)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a.v.x, 1.0f, true)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a.v.y, 1.0f, false)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a.v.y, 1.0f, true)));
 }
 
-template <typename TS> __device__ __forceinline__ f32x4 load_scales(const TS* p);
-template <> __device__ __forceinline__ f32x4 load_scales<float>(const float* p) {
-  return *reinterpret_cast<const f32x4*>(p);
-}
-template <> __device__ __forceinline__ f32x4 load_scales<uint16_t>(const uint16_t* p) {
+__device__ __forceinline__ f32x4 load_scales(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+__device__ __forceinline__ f32x4 load_scales(const uint16_t* p) {
   const uint2 v = *reinterpret_cast<const uint2*>(p);
   return f32x4{__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
                __uint_as_float(v.y & 0xffff0000u)};
+}
+
+// the value that lane LANE of this lane's 16-lane row holds
+template <int LANE> __device__ __forceinline__ float row_bcast(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x150 + LANE, 0xF, 0xF, true));
 }
 
 struct GemvArgs {
@@ -125,143 +126,298 @@ struct GemvArgs {
   const int32_t* offsets;
   int64_t rows_cap;
   int N, K;
+  int waves;                                    // of a workgroup
+  int split;                                    // waves that share a column block's stages
+  int silu, out_f32;
   void* out;
-  int out_f32;
 };
 
-constexpr int kPad = 4;                                   // LDS row padding, floats
+constexpr int kPad = 4;                         // LDS row padding, floats
 constexpr int kRedStride = kTiles * 16 + kPad;
 
-// One block of at most 16 * MT rows against the workgroup's 64 weight rows.
-template <int FMT, bool FP8, typename TS, int SG, bool SILU, int MT>
-__device__ __forceinline__ void rows_block(const GemvArgs& p, int e, int nb, int64_t row0, int rows, float* red) {
-  const int lane = moe::lane_id(), wave = threadIdx.x >> 6;
-  const int n = lane & 15, j = lane >> 4;
-  const int KS = p.K / 128;
-  constexpr int ESZ = FP8 ? 1 : 2;
-  // the workgroup's tiles: 64 rows of G, or 32 gate and the 32 up rows they pair with
-  int64_t tile[kTiles];
-#pragma unroll
-  for (int f = 0; f < kTiles; ++f) {
-    const int64_t base = static_cast<int64_t>(e) * (p.N / 16);
-    tile[f] = SILU ? base + (f >> 1) * (p.N / 32) + nb * 2 + (f & 1) : base + nb * 4 + f;
-  }
-  const TS* scales = static_cast<const TS*>(p.scales);
-  f32x4 acc[kTiles][MT];
-#pragma unroll
-  for (int f = 0; f < kTiles; ++f)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[f][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+// One column block (four weight tiles) of one expert, for one wave.
+//
+// Lane 16 j + n holds, of every 16 x 16 result, weight rows 4 j .. 4 j + 3 and
+// activation row n, so all 16 lanes of a row of lanes need the same scales.
+// They share one load: lane n fetches the four scales of tile n & 3 and of the
+// (n >> 2)-th group from here on, and the folds read them by row broadcasts,
+// which are operand modifiers of the multiply-add.
+template <int FMT, bool FP8, typename TS, int SG, int MT> struct Block {
+  static constexpr int ESZ = FP8 ? 1 : 2;
+  static constexpr int SPG = 4 / SG;            // 32-column steps of a scale group
+  static constexpr int CH = 4 / SG;             // stages that one scale load covers
+  static constexpr int UN = CH < 2 ? 2 : CH;    // stages of the unrolled loop
 
-  const bf16x8 minus24 = as_bf16x8(0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u);
-  constexpr int SPG = 4 / SG;                              // 32-column steps per group
-  for (int ks = wave; ks < KS; ks += kWaves) {
+  // Up to 16 rows, a stage's weights and activations are fetched one stage
+  // ahead (weights three stages ahead at two waves per SIMD: the same time to
+  // 1 % for one or four rows, 2 to 8 % more on the down shape); 32 rows leave
+  // no registers for the activations (168 at three waves per SIMD), which are
+  // fetched when their stage begins.
+  static constexpr bool kAhead = MT == 1;
+  struct Rows {
+    Act<FP8> act[MT][4];
+    float as[MT];
+  };
+  struct Buf {                                  // one stage's weights
     uint4 w[kTiles];
-    f32x4 sc[kTiles][SG];
-#pragma unroll
-    for (int f = 0; f < kTiles; ++f) {
-      w[f] = *reinterpret_cast<const uint4*>(p.codes + ((tile[f] * KS + ks) * 64 + lane) * 16);
-#pragma unroll
-      for (int g = 0; g < SG; ++g) sc[f][g] = load_scales<TS>(scales + ((tile[f] * KS + ks) * SG + g) * 16 + j * 4);
-    }
+  };
+
+  const uint8_t* w[kTiles];                     // uniform
+  const uint8_t* ap[MT];
+  const float* asp[MT];
+  const TS* sp;
+  int KS, usub, lane;
+  f32x4 acc[kTiles][MT];
+
+  __device__ __forceinline__ void load_rows(Rows& r, int ks) const {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const int r = m * 16 + n;
-      const bool live = r < rows;
-      const uint8_t* ap = p.a + ((row0 + r) * p.K + ks * 128 + j * 8) * ESZ;
-      bf16x8 act[4];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) act[s] = live ? load_act<FP8>(ap + s * 32 * ESZ) : as_bf16x8(0, 0, 0, 0);
-      const float as = FP8 ? (live ? p.a_scales[(row0 + r) * KS + ks] : 0.f) : 1.f;
+      for (int s = 0; s < 4; ++s)
+        r.act[m][s] = *reinterpret_cast<const Act<FP8>*>(ap[m] + static_cast<int64_t>(ks) * (128 * ESZ) + s * 32 * ESZ);
+      if constexpr (FP8) r.as[m] = asp[m][ks];
+    }
+  }
+  __device__ __forceinline__ void load(Buf& b, int ks) const {
 #pragma unroll
-      for (int g = 0; g < SG; ++g) {
-        f32x4 c0 = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (FMT == MOE_W4_INT4) {
+    for (int f = 0; f < kTiles; ++f) b.w[f] = moe::load_nt16(w[f] + static_cast<int64_t>(ks) * 1024 + lane * 16);
+  }
+  __device__ __forceinline__ f32x4 scales(int ks) const {
+    const int k = min(ks + usub, KS - 1);
+    return load_scales(sp + static_cast<int64_t>(k) * (SG * 16));
+  }
+
+  template <int SUB, int G, int F> __device__ __forceinline__ void fold(const f32x4& sc, const Rows& r, int m, const f32x4& c) {
 #pragma unroll
-          for (int s = 0; s < SPG; ++s)
-            c0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(minus24, act[g * SPG + s], c0, 0, 0, 0);
-        }
+    for (int i = 0; i < 4; ++i) {
+      const float v = FP8 ? c[i] * r.as[m] : c[i];
+      acc[F][m][i] = fmaf(row_bcast<(SUB * SG + G) * 4 + F>(sc[i]), v, acc[F][m][i]);
+    }
+  }
+  static __device__ __forceinline__ uint32_t dword(const uint4& v, int d) {
+    return d == 0 ? v.x : d == 1 ? v.y : d == 2 ? v.z : v.w;
+  }
+
+  template <int SUB, int G> __device__ __forceinline__ void group(const f32x4& sc, const Buf& b, const Rows& r) {
+    f32x4 c0[MT];
 #pragma unroll
-        for (int f = 0; f < kTiles; ++f) {
-          const uint32_t d[4] = {w[f].x, w[f].y, w[f].z, w[f].w};
-          f32x4 c = c0;
+    for (int m = 0; m < MT; ++m) {
+      c0[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if constexpr (FMT == MOE_W4_INT4) {
+        const bf16x8 minus24 = as_bf16x8(0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u);
 #pragma unroll
-          for (int s = 0; s < SPG; ++s)
-            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(unpack<FMT>(d[g * SPG + s]), act[g * SPG + s], c, 0, 0, 0);
+        for (int s = 0; s < SPG; ++s)
+          c0[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(minus24, act_bf16(r.act[m][G * SPG + s]), c0[m], 0, 0, 0);
+      }
+    }
+    if constexpr (MT == 1) {
+      // the four tiles side by side: four independent chains of products
+      f32x4 c[kTiles] = {c0[0], c0[0], c0[0], c0[0]};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[f][m][i] = fmaf(c[i], FP8 ? sc[f][g][i] * as : sc[f][g][i], acc[f][m][i]);
-        }
+      for (int s = 0; s < SPG; ++s)
+#pragma unroll
+        for (int f = 0; f < kTiles; ++f)
+          c[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(unpack<FMT>(dword(b.w[f], G * SPG + s)),
+                                                         act_bf16(r.act[0][G * SPG + s]), c[f], 0, 0, 0);
+      fold<SUB, G, 0>(sc, r, 0, c[0]);
+      fold<SUB, G, 1>(sc, r, 0, c[1]);
+      fold<SUB, G, 2>(sc, r, 0, c[2]);
+      fold<SUB, G, 3>(sc, r, 0, c[3]);
+    } else {
+      tile<SUB, G, 0>(sc, b, r, c0);
+      tile<SUB, G, 1>(sc, b, r, c0);
+      tile<SUB, G, 2>(sc, b, r, c0);
+      tile<SUB, G, 3>(sc, b, r, c0);
+    }
+  }
+  template <int SUB, int G, int F>
+  __device__ __forceinline__ void tile(const f32x4& sc, const Buf& b, const Rows& r, const f32x4 (&c0)[MT]) {
+    f32x4 c[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) c[m] = c0[m];
+#pragma unroll
+    for (int s = 0; s < SPG; ++s) {
+      const bf16x8 v = unpack<FMT>(dword(b.w[F], G * SPG + s));
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        c[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, act_bf16(r.act[m][G * SPG + s]), c[m], 0, 0, 0);
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) fold<SUB, G, F>(sc, r, m, c[m]);
+    __builtin_amdgcn_sched_barrier(0);          // one tile's products at a time
+  }
+
+  template <int SUB> __device__ __forceinline__ void stage(const f32x4& sc, const Buf& b, const Rows& r) {
+    group<SUB, 0>(sc, b, r);
+    if constexpr (SG >= 2) group<SUB, 1>(sc, b, r);
+    if constexpr (SG == 4) {
+      group<SUB, 2>(sc, b, r);
+      group<SUB, 3>(sc, b, r);
+    }
+  }
+
+  // Step U of the unrolled loop: the next stage's loads, then this stage.
+  // Loads return in order, so those that are needed sooner go first.
+  template <int U, typename KsOf>
+  __device__ __forceinline__ void step(int i, int n, const KsOf& ks_of, f32x4& sc, f32x4& sc_next, Buf (&b)[2],
+                                       Rows (&r)[2]) {
+    if (i >= n) return;
+    if constexpr (U % CH == 0) {
+      sc = sc_next;
+      if (i + CH < n) sc_next = scales(ks_of(i + CH));
+    }
+    if constexpr (kAhead) {
+      if (i + 1 < n) load_rows(r[(U + 1) & 1], ks_of(i + 1));
+    } else {
+      load_rows(r[0], ks_of(i));
+    }
+    if (i + 1 < n) load(b[(U + 1) & 1], ks_of(i + 1));
+    __builtin_amdgcn_sched_barrier(0);
+    stage<U % CH>(sc, b[U & 1], r[kAhead ? U & 1 : 0]);
+  }
+
+  // The sums of rows row0 .. row0 + rows - 1 (rows <= 16 MT) over the wave's
+  // share of the stages: chunks part, part + split, ... of CH stages.
+  __device__ __forceinline__ void products(const GemvArgs& p, int e, int nb, int part, int64_t row0, int rows) {
+    lane = moe::lane_id();
+    const int n = lane & 15, j = lane >> 4;
+    KS = p.K / 128;
+    auto tile = [&](int f) {   // 64 rows of G, or 32 gate rows and the 32 up rows they pair with
+      return static_cast<int64_t>(e) * (p.N / 16) + (p.silu ? (f >> 1) * (p.N / 32) + nb * 2 + (f & 1) : nb * 4 + f);
+    };
+#pragma unroll
+    for (int f = 0; f < kTiles; ++f) w[f] = p.codes + tile(f) * KS * 1024;
+    const int u = n >> 2;
+    usub = u / SG;
+    sp = static_cast<const TS*>(p.scales) + (tile(n & 3) * KS * SG + u % SG) * 16 + j * 4;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      // lanes past the last row read row 0 again; what they compute is not stored
+      const int64_t r = row0 + (m * 16 + n < rows ? m * 16 + n : 0);
+      ap[m] = p.a + (r * p.K + j * 8) * ESZ;
+      if constexpr (FP8) asp[m] = p.a_scales + r * KS;
+#pragma unroll
+      for (int f = 0; f < kTiles; ++f) acc[f][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    const int NC = (KS + CH - 1) / CH;
+    const int own = part < NC ? (NC - part + p.split - 1) / p.split : 0;
+    const bool last = own > 0 && (own - 1) * p.split + part == NC - 1;
+    const int count = own * CH - (last ? NC * CH - KS : 0);
+    auto ks_of = [&](int i) { return ((i / CH) * p.split + part) * CH + i % CH; };
+    if (count == 0) return;
+    Buf b[2];
+    Rows r[2];
+    f32x4 sc, sc_next = scales(ks_of(0));
+    if constexpr (kAhead) load_rows(r[0], ks_of(0));
+    load(b[0], ks_of(0));
+    for (int i = 0; i < count; i += UN) {
+      step<0>(i, count, ks_of, sc, sc_next, b, r);
+      step<1>(i + 1, count, ks_of, sc, sc_next, b, r);
+      if constexpr (UN == 4) {
+        step<2>(i + 2, count, ks_of, sc, sc_next, b, r);
+        step<3>(i + 3, count, ks_of, sc, sc_next, b, r);
       }
     }
   }
 
-  // the four waves' sums, in wave order, 16 rows at a time
-  constexpr int COLS = SILU ? 32 : 64;
-  constexpr int QUADS = COLS / 4;
-  const int ldo = SILU ? p.N / 2 : p.N;
+  // The waves' sums through LDS, in wave order, 16 rows at a time, and the
+  // epilogue.  With split 1 a wave only meets itself.
+  __device__ __forceinline__ void store(const GemvArgs& p, int nb, int part, int64_t row0, int rows, float* mine) const {
+    const int n = lane & 15, j = lane >> 4;
+    const int cols = p.silu ? 32 : 64, quads = cols / 4;
+    const int ldo = p.silu ? p.N / 2 : p.N;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    __syncthreads();
+    for (int m = 0; m < MT; ++m) {
+      if (p.split > 1) __syncthreads();
 #pragma unroll
-    for (int f = 0; f < kTiles; ++f)
-      *reinterpret_cast<f32x4*>(red + (wave * 16 + n) * kRedStride + f * 16 + j * 4) = acc[f][m];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * QUADS; i += kThreads) {
-      const int r = i / QUADS, q = i % QUADS * 4;
-      if (m * 16 + r >= rows) continue;
-      f32x4 v = {0.f, 0.f, 0.f, 0.f}, u = v;
+      for (int f = 0; f < kTiles; ++f)
+        *reinterpret_cast<f32x4*>(mine + (part * 16 + n) * kRedStride + f * 16 + j * 4) = acc[f][m];
+      if (p.split > 1) __syncthreads();
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      for (int i = part * MOE_WAVE + lane; i < 16 * quads; i += p.split * MOE_WAVE) {
+        const int r = i / quads, q = i % quads * 4;
+        if (m * 16 + r >= rows) break;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f}, u = v;
+        for (int s = 0; s < p.split; ++s) {
+          const float* src = mine + (s * 16 + r) * kRedStride + q;
+          v += *reinterpret_cast<const f32x4*>(src);
+          if (p.silu) u += *reinterpret_cast<const f32x4*>(src + 32);
+        }
+        if (p.silu) {
 #pragma unroll
-      for (int s = 0; s < kWaves; ++s) {
-        const float* src = red + (s * 16 + r) * kRedStride + q;
-        v += *reinterpret_cast<const f32x4*>(src);
-        if constexpr (SILU) u += *reinterpret_cast<const f32x4*>(src + 32);
+          for (int k = 0; k < 4; ++k) v[k] = moe::silu(v[k]) * u[k];
+        }
+        const int64_t at = (row0 + m * 16 + r) * ldo + nb * cols + q;
+        if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+        else
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+              make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
       }
-      if constexpr (SILU) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = moe::silu(v[k]) * u[k];
-      }
-      const int64_t at = (row0 + m * 16 + r) * ldo + nb * COLS + q;
-      if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
-      else
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
-            make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
     }
   }
-}
-
-template <int FMT, bool FP8, typename TS, int SG, bool SILU>
-__global__ __launch_bounds__(kThreads) void gemv_w4_kernel(GemvArgs p) {
-  __shared__ float red[kWaves * 16 * kRedStride];
-  const int nbs = p.N / 64;
-  const int e = blockIdx.x / nbs, nb = blockIdx.x % nbs;
-  const int64_t off = p.offsets[e];
-  int64_t rows = p.counts[e];
-  if (off < 0) return;
-  if (rows > p.rows_cap - off) rows = p.rows_cap - off;
-  for (int64_t r = 0; r < rows; r += 64) {
-    const int m = static_cast<int>(rows - r < 64 ? rows - r : 64);
-    if (m <= 16) rows_block<FMT, FP8, TS, SG, SILU, 1>(p, e, nb, off + r, m, red);
-    else if (m <= 32) rows_block<FMT, FP8, TS, SG, SILU, 2>(p, e, nb, off + r, m, red);
-    else rows_block<FMT, FP8, TS, SG, SILU, 4>(p, e, nb, off + r, m, red);
-  }
-}
+};
 
 template <int FMT, bool FP8, typename TS, int SG>
-void launch_epi(const GemvArgs& p, int L, bool silu, hipStream_t stream) {
-  const int grid = L * (p.N / 64);
-  if (silu) gemv_w4_kernel<FMT, FP8, TS, SG, true><<<grid, kThreads, 0, stream>>>(p);
-  else gemv_w4_kernel<FMT, FP8, TS, SG, false><<<grid, kThreads, 0, stream>>>(p);
+__global__ __launch_bounds__(kMaxWaves * MOE_WAVE, 3) void gemv_w4_kernel(GemvArgs p) {
+  extern __shared__ float red[];                            // [waves][16][kRedStride]
+  const int nbs = p.N / 64, blocks = p.waves / p.split;      // column blocks of an expert, of this workgroup
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = wave / p.split, part = wave % p.split;
+  const int per = (nbs + blocks - 1) / blocks;
+  const int e = blockIdx.x / per, nb = (blockIdx.x % per) * blocks + group;
+  // nb is the same for all waves that meet at a barrier
+  const int64_t off = p.offsets[e];
+  int64_t rows = p.counts[e];
+  if (off < 0 || nb >= nbs) return;
+  if (rows > p.rows_cap - off) rows = p.rows_cap - off;
+  float* mine = red + group * p.split * 16 * kRedStride;
+  for (int64_t r = 0; r < rows; r += 32) {
+    const int m = static_cast<int>(rows - r < 32 ? rows - r : 32);
+    if (m <= 16) {
+      Block<FMT, FP8, TS, SG, 1> w;
+      w.products(p, e, nb, part, off + r, m);
+      w.store(p, nb, part, off + r, m, mine);
+    } else {
+      Block<FMT, FP8, TS, SG, 2> w;
+      w.products(p, e, nb, part, off + r, m);
+      w.store(p, nb, part, off + r, m, mine);
+    }
+  }
 }
+
+// How many waves share a column block: up to four while each keeps eight
+// stages (a wave's first loads and the sums' meeting cost about four stages'
+// time), and up to eight with four stages each where the blocks would not fill
+// the card's SIMDs once.  Measured with four rows an expert, in us, for 1 / 2 /
+// 4 / 8 waves: L 32, 4096 x 7168: 96 / 92 / 87 / 109; L 32, 7168 x 2048: 55 / 48 /
+// 56 / 91; L 64, 4096 x 1408: 36 / 40 / 46 / 92; L 1, 4096 x 7168: 52 / 28 / 18 / 14;
+// L 1, 7168 x 2048: 17 / 11 / 7.8 / 7.9.
+void pick_split(GemvArgs& p, int L) {
+  const int KS = p.K / 128;
+  const int64_t blocks = static_cast<int64_t>(L) * (p.N / 64);
+  p.split = 1;
+  while (p.split < 4 && KS >= 16 * p.split) p.split *= 2;
+  while (p.split < kMaxWaves && KS >= 8 * p.split && blocks * p.split <= kSimds) p.split *= 2;
+  p.waves = p.split > 4 ? p.split : 4;
+}
+
 template <int FMT, bool FP8, typename TS>
-void launch_group(const GemvArgs& p, int L, int group, bool silu, hipStream_t stream) {
-  if (group == 128) launch_epi<FMT, FP8, TS, 1>(p, L, silu, stream);
-  else if (group == 64) launch_epi<FMT, FP8, TS, 2>(p, L, silu, stream);
-  else launch_epi<FMT, FP8, TS, 4>(p, L, silu, stream);
+void launch_group(const GemvArgs& a, int L, int group, hipStream_t stream) {
+  GemvArgs p = a;
+  pick_split(p, L);
+  const int nbs = p.N / 64, blocks = p.waves / p.split;
+  const int grid = L * ((nbs + blocks - 1) / blocks), threads = p.waves * MOE_WAVE;
+  const size_t lds = static_cast<size_t>(p.waves) * 16 * kRedStride * sizeof(float);
+  if (group == 128) gemv_w4_kernel<FMT, FP8, TS, 1><<<grid, threads, lds, stream>>>(p);
+  else if (group == 64) gemv_w4_kernel<FMT, FP8, TS, 2><<<grid, threads, lds, stream>>>(p);
+  else gemv_w4_kernel<FMT, FP8, TS, 4><<<grid, threads, lds, stream>>>(p);
 }
-template <int FMT, bool FP8>
-void launch_scale(const GemvArgs& p, int L, bool s32, int group, bool silu, hipStream_t stream) {
-  if (s32) launch_group<FMT, FP8, float>(p, L, group, silu, stream);
-  else launch_group<FMT, FP8, uint16_t>(p, L, group, silu, stream);
+template <int FMT, bool FP8> void launch_scale(const GemvArgs& p, int L, bool s32, int group, hipStream_t stream) {
+  if (s32) launch_group<FMT, FP8, float>(p, L, group, stream);
+  else launch_group<FMT, FP8, uint16_t>(p, L, group, stream);
 }
 
 inline bool w4_sizes(int L, int N, int K) { return L >= 1 && N >= 1 && K >= 1; }
@@ -314,15 +470,15 @@ extern "C" moe_status moe_grouped_gemv_w4(const void* a, moe_dtype a_dt, const f
   MOE_CHECK(a_dt != MOE_FP8_E4M3 || a_scales, MOE_ERR_INVALID_ARG);
   MOE_CHECK(aligned16(a) && aligned16(codes_packed) && aligned16(scales_packed) && aligned16(out), MOE_ERR_INVALID_ARG);
   const GemvArgs p{static_cast<const uint8_t*>(a), a_scales, static_cast<const uint8_t*>(codes_packed), scales_packed,
-                   counts, offsets, rows_cap, N, K, out, out_dt == MOE_F32};
-  const bool silu = epi == MOE_EPI_SILU_MUL, s32 = s_dt == MOE_F32;
+                   counts, offsets, rows_cap, N, K, 4, 4, epi == MOE_EPI_SILU_MUL, out_dt == MOE_F32, out};
+  const bool s32 = s_dt == MOE_F32;
   const bool fp8 = a_dt == MOE_FP8_E4M3;
   if (fmt == MOE_W4_INT4) {
-    if (fp8) launch_scale<MOE_W4_INT4, true>(p, L, s32, group, silu, stream);
-    else launch_scale<MOE_W4_INT4, false>(p, L, s32, group, silu, stream);
+    if (fp8) launch_scale<MOE_W4_INT4, true>(p, L, s32, group, stream);
+    else launch_scale<MOE_W4_INT4, false>(p, L, s32, group, stream);
   } else {
-    if (fp8) launch_scale<MOE_W4_E2M1, true>(p, L, s32, group, silu, stream);
-    else launch_scale<MOE_W4_E2M1, false>(p, L, s32, group, silu, stream);
+    if (fp8) launch_scale<MOE_W4_E2M1, true>(p, L, s32, group, stream);
+    else launch_scale<MOE_W4_E2M1, false>(p, L, s32, group, stream);
   }
   MOE_LAUNCH_CHECK();
   return MOE_OK;

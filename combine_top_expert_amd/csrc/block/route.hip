@@ -1,16 +1,20 @@
 // moe_router_group_topk and its backward.
 //
-// One wavefront per token; lane l holds experts l, l + 64, ...  A score c =
-// s + bias is held as the order-preserving 32-bit key of the router's top-K
-// (NaN lowest among the live, 0 for a masked or retired entry), so a selection
-// round is a wave maximum and a ballot for its lowest holder.
+// One wavefront per token; lane l holds the NPL neighbours l NPL, l NPL + 1, ...
+// so a row is read with one wide load per lane and a group of experts is
+// usually a run of lanes, whose two best scores meet in a few DPP steps.  A
+// score c = s + bias is held as the order-preserving 32-bit key of the router's
+// top-K (NaN lowest among the live, 0 for a masked or retired entry).  Every
+// lane sorts its keys once; a selection round is then a wave maximum of the
+// lanes' heads, a ballot for the lowest lane that holds it, and a shift of that
+// lane's list.  Lanes are in expert order and the sort is stable, so equal keys
+// go to the lower id.
 //
 // The order is the one of exact scores.  Without a bias it is the logits' order,
 // which needs no arithmetic.  Where arithmetic decides (a bias, or the sums that
-// rank the groups), an fp32 score is off by at most kRel 2^-24 of the row's
-// largest score plus the rounding of the bias's addition; a row in which two
-// neighbours of the order lie within that of each other is decided again by
-// the same wave in fp64 (route_exact).
+// rank the groups), an fp32 score is off by at most a few 2^-24 of the row's
+// scores; a row in which two neighbours of the order lie within that of each
+// other is decided again by the same wave in fp64 (route_exact).
 
 #include "block_common.h"
 #include "router_common.h"
@@ -28,11 +32,7 @@ constexpr int kWaves = kThreads / MOE_WAVE;
 constexpr int kMaxE = 1024;
 constexpr int kMaxK = 32;
 constexpr float kMask = -3.3e38f;   // covers -inf and the lowest finite fp32 and bf16
-// expf 1 ulp, the sum of the softmax (64 lanes x 16 terms, a tree: 22
-// roundings of positive terms), l - max one rounding whose effect on e is at
-// most 0.37 2^-24 of the largest e, one addition and one division: below 28
-// half-ulps.
-constexpr float kRel = 32.0f * 5.9604644775390625e-8f;
+constexpr float kU = 5.9604644775390625e-8f;   // 2^-24, half a step of fp32
 
 struct RouteArgs {
   const float* logits;
@@ -42,6 +42,7 @@ struct RouteArgs {
   int n_group, topk_group, group_top, group_size;
   int renorm;
   float scale;
+  int vec;                      // rows may be read NPL logits at a time
   int32_t* ids;
   float* weights;
 };
@@ -131,6 +132,38 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, const float* __restr
   return my;
 }
 
+// exp(d) by the hardware's exp2: within (1.1 |d| + 2) kU of itself
+__device__ __forceinline__ float fast_exp(float d) { return __builtin_amdgcn_exp2f(d * 1.44269504088896341f); }
+
+// Sorts K[0..N) descending, I along with it (odd-even transposition for two,
+// else a merge network); keys of equal value keep their order.
+template <int N> __device__ __forceinline__ void sort_desc(uint32_t (&k)[N], int (&id)[N]) {
+  // stable: an exchange only where the later key is strictly larger, between
+  // neighbours; N is small and the network unrolled
+#pragma unroll
+  for (int pass = 0; pass < N; ++pass)
+#pragma unroll
+    for (int i = pass & 1; i + 1 < N; i += 2) {
+      const bool sw = k[i + 1] > k[i];
+      const uint32_t hi = max(k[i], k[i + 1]), lo = min(k[i], k[i + 1]);
+      const int a = sw ? id[i + 1] : id[i], b = sw ? id[i] : id[i + 1];
+      k[i] = hi; k[i + 1] = lo;
+      id[i] = a; id[i + 1] = b;
+    }
+}
+
+// (t1, t2) <- the two largest of this lane's and its partner's
+template <int CTRL> __device__ __forceinline__ void merge2(uint32_t& t1, uint32_t& t2) {
+  const uint32_t o1 = moe_router::dpp_u32<CTRL>(t1, t1), o2 = moe_router::dpp_u32<CTRL>(t2, t2);
+  t2 = max(min(t1, o1), max(t2, o2));
+  t1 = max(t1, o1);
+}
+__device__ __forceinline__ void merge2_shfl(uint32_t& t1, uint32_t& t2, int d) {
+  const uint32_t o1 = __shfl_xor(t1, d), o2 = __shfl_xor(t2, d);
+  t2 = max(min(t1, o1), max(t2, o2));
+  t1 = max(t1, o1);
+}
+
 template <int NPL>   // scores per lane: E <= 64 * NPL
 __global__ __launch_bounds__(kThreads) void group_topk_kernel(RouteArgs a) {
   extern __shared__ double lds[];
@@ -139,16 +172,34 @@ __global__ __launch_bounds__(kThreads) void group_topk_kernel(RouteArgs a) {
   const int t = blockIdx.x * kWaves + wave;
   if (t >= a.T) return;
   const float* row = a.logits + static_cast<int64_t>(t) * a.E;
-  double* c64 = lds + static_cast<size_t>(wave) * a.E;
-  float* c32 = reinterpret_cast<float*>(c64);
+  const int e0 = lane * NPL;
 
-  float l[NPL];
+  float l[NPL], b[NPL];
+  if (NPL > 1 && a.vec) {
+    typedef float vec_t __attribute__((ext_vector_type(NPL < 4 ? NPL : 4)));
+    constexpr int W = NPL < 4 ? NPL : 4;
 #pragma unroll
-  for (int j = 0; j < NPL; ++j) {
-    const int e = lane + MOE_WAVE * j;
-    l[j] = e < a.E ? row[e] : -INFINITY;
+    for (int j = 0; j < NPL; j += W) {
+      vec_t v = {}, w = {};
+      if (e0 < a.E) {
+        v = *reinterpret_cast<const vec_t*>(row + e0 + j);
+        if (a.bias) w = *reinterpret_cast<const vec_t*>(a.bias + e0 + j);
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        l[j + i] = e0 < a.E ? v[i] : -INFINITY;
+        b[j + i] = w[i];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) {
+      l[j] = e0 + j < a.E ? row[e0 + j] : -INFINITY;
+      b[j] = a.bias && e0 + j < a.E ? a.bias[e0 + j] : 0.f;
+    }
   }
-  float m = 0.f, sum = 1.f;
+
+  float m = 0.f, sum = 1.f, inv = 1.f;
   if (!a.sigmoid) {
     m = -INFINITY;
 #pragma unroll
@@ -158,122 +209,163 @@ __global__ __launch_bounds__(kThreads) void group_topk_kernel(RouteArgs a) {
     sum = 0.f;
 #pragma unroll
     for (int j = 0; j < NPL; ++j)
-      if (!(l[j] <= kMask)) sum += expf(l[j] - m);
+      if (!(l[j] <= kMask)) sum += fast_exp(l[j] - m);
     sum = wave_sum_f32(sum);
+    inv = 1.0f / sum;
   }
-  auto score = [&](float x) { return a.sigmoid ? sigmoid_f(x) : (x <= kMask ? 0.f : expf(x - m) / sum); };
+  auto fast_score = [&](float x) {
+    return a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-x)) : fast_exp(x - m) * inv;
+  };
 
-  // keys: of the logits without a bias, of c with one
+  // Keys: of the logits without a bias, of c with one.  fast_score is off by at
+  // most (1.1 |d| + 2 + 1 + 2) kU of itself (d: the exponent; exp, add and
+  // reciprocal), for softmax by the sum's and the quotient's roundings too
+  // (NPL + 6 additions, terms that are off by 5 kU on average at most).
+  const float c0 = a.sigmoid ? 6.f : 20.f + NPL;
   uint32_t key[NPL];
-  float smax = 0.f, cmax = 0.f;
+  int id[NPL];
+  float err = 0.f;
 #pragma unroll
   for (int j = 0; j < NPL; ++j) {
-    const int e = lane + MOE_WAVE * j;
     key[j] = 0;
-    if (e < a.E && !(l[j] <= kMask)) {
-      float v = l[j];
-      if (a.bias) {
-        const float b = a.bias[e], s = score(l[j]);
-        v = s + b;
-        if (!(b <= kMask)) {
-          key[j] = max(score_key(v), 1u);
-          smax = fmaxf(smax, s);
-          if (fabsf(v) < INFINITY) cmax = fmaxf(cmax, fabsf(v));
-        }
-      } else {
-        key[j] = (sum != sum) ? 1u : max(score_key(v), 1u);
+    id[j] = e0 + j;
+    const bool live = !(l[j] <= kMask);
+    if (a.bias) {
+      const float s = fast_score(l[j]), v = s + b[j];
+      if (live && !(b[j] <= kMask)) {
+        key[j] = max(score_key(v), 1u);
+        const float d = a.sigmoid ? l[j] : l[j] - m;
+        err = fmaxf(err, fmaf(s, fmaf(1.5f, fabsf(d), c0), fabsf(v) < INFINITY ? fabsf(v) : 0.f));
       }
+    } else if (live) {
+      key[j] = sum != sum ? 1u : max(score_key(l[j]), 1u);
     }
   }
-  // how far an fp32 c may be off (0 without a bias: logits are exact)
-  float tol = 0.f;
-  if (a.bias) tol = kRel * wave_max_f32(smax) + 1.2e-7f * wave_max_f32(cmax);
+  // how far a c may be off: 0 without a bias, where keys are exact
+  const float tol = a.bias ? wave_max_f32(err) * kU : 0.f;
 
   bool near = false;
   if (a.n_group > 1) {
+    const int gs = a.group_size;
+    const int lg = gs / NPL;                            // lanes of a group
+    const bool runs = gs % NPL == 0 && (lg & (lg - 1)) == 0;
+    uint32_t t1 = 0, t2 = 0;
+    int g, stride;                                      // this lane's group, lanes between groups
+    if (runs) {
 #pragma unroll
-    for (int j = 0; j < NPL; ++j) {
-      const int e = lane + MOE_WAVE * j;
-      if (e < a.E) c32[e] = __uint_as_float(key[j]);
+      for (int j = 0; j < NPL; ++j) {
+        t2 = max(t2, min(t1, key[j]));
+        t1 = max(t1, key[j]);
+      }
+      if (lg >= 2) merge2<moe_router::kDppXor1>(t1, t2);
+      if (lg >= 4) merge2<moe_router::kDppXor2>(t1, t2);
+      if (lg >= 8) merge2<moe_router::kDppHalfMirror>(t1, t2);
+      if (lg >= 16) merge2<moe_router::kDppMirror>(t1, t2);
+      if (lg >= 32) merge2_shfl(t1, t2, 16);
+      if (lg >= 64) merge2_shfl(t1, t2, 32);
+      g = lane >> __builtin_ctz(lg);
+      stride = lg;
+    } else {
+      uint32_t* c32 = reinterpret_cast<uint32_t*>(lds + static_cast<size_t>(wave) * a.E);
+#pragma unroll
+      for (int j = 0; j < NPL; ++j)
+        if (e0 + j < a.E) c32[e0 + j] = key[j];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (lane < a.n_group)
+        for (int i = 0; i < gs; ++i) {
+          const uint32_t k = c32[lane * gs + i];
+          t2 = max(t2, min(t1, k));
+          t1 = max(t1, k);
+        }
+      g = lane;
+      stride = 1;
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    // the group's score; dead groups keep key 0
     uint32_t gkey = 0;
-    float gs = -INFINITY;
-    if (lane < a.n_group) {
-      uint32_t k1 = 0, k2 = 0;
-      for (int i = 0; i < a.group_size; ++i) {
-        const uint32_t k = __float_as_uint(c32[lane * a.group_size + i]);
-        k2 = max(k2, min(k1, k));
-        k1 = max(k1, k);
+    if (t1 && g < a.n_group) {
+      float v = key_value(t1);
+      if (a.group_top == 2) {
+        if (!a.bias) v = fast_score(v);
+        if (t2) v += a.bias ? key_value(t2) : fast_score(key_value(t2));
       }
-      if (k1) {
-        const bool two = a.group_top == 2 && k2;
-        gs = key_value(k1);
-        if (!a.bias && a.group_top == 2) gs = score(gs);
-        if (two) gs += a.bias ? key_value(k2) : score(key_value(k2));
-        gkey = max(score_key(gs), 1u);
+      gkey = max(score_key(v), 1u);
+    }
+    int rank = 0;
+    for (int h = 0; h < a.n_group; ++h) {
+      const uint32_t o = __builtin_amdgcn_readlane(gkey, h * stride);
+      rank += (o > gkey || (o == gkey && h < g)) ? 1 : 0;
+    }
+    const bool kept = g < a.n_group && rank < a.topk_group;
+    // the last group that stays and the first that does not
+    const uint64_t in = __ballot(g < a.n_group && rank == a.topk_group - 1);
+    const uint64_t out = __ballot(g < a.n_group && rank == a.topk_group);
+    if (out && (a.bias || a.group_top == 2)) {
+      const uint32_t ki = __builtin_amdgcn_readlane(gkey, __builtin_ctzll(in));
+      const uint32_t ko = __builtin_amdgcn_readlane(gkey, __builtin_ctzll(out));
+      if (ki > 1 && ko > 1) {
+        const float vi = key_value(ki), vo = key_value(ko);
+        // without a bias a sum of two scores is off by its own share
+        // (exponents to 88) and by what fp32 loses below its normal range
+        near = vi - vo <= (a.bias ? 4.f * tol + 2.f * kU * (fabsf(vi) + fabsf(vo)) : (c0 + 140.f) * kU * (vi + vo) + 1e-37f);
       }
     }
-    uint64_t keep = 0;
-    float last = 0.f;
-    for (int g = 0; g <= a.topk_group; ++g) {
-      const bool in = lane < a.n_group && !((keep >> lane) & 1);
-      const uint32_t win = wave_max_u32(in ? gkey : 0u);
-      const uint64_t holders = __ballot(in && gkey == win);
-      if (!holders || win == 0) break;
-      const float v = key_value(win);
-      if (g == a.topk_group) {      // the best group that stays out
-        // without a bias a group's sum is off by kRel of itself (1e-37: what
-        // fp32 loses below its normal range); a single logit is exact
-        if (a.bias) near = last - v <= 4.f * tol;
-        else if (a.group_top == 2) near = last - v <= kRel * (last + v) + 1e-37f;
-        break;
-      }
-      keep |= holders & (~holders + 1);
-      last = v;
-    }
+    if (runs) {
 #pragma unroll
-    for (int j = 0; j < NPL; ++j) {
-      const int e = lane + MOE_WAVE * j;
-      if (e < a.E && !((keep >> (e / a.group_size)) & 1)) key[j] = 0;
+      for (int j = 0; j < NPL; ++j) key[j] = kept ? key[j] : 0u;
+    } else {
+      const uint64_t keep = __ballot(kept);
+#pragma unroll
+      for (int j = 0; j < NPL; ++j)
+        if (e0 + j < a.E && !((keep >> ((e0 + j) / gs)) & 1)) key[j] = 0;
     }
   }
 
   int my = -1;
-  float last = INFINITY;
   if (!near) {
+    sort_desc<NPL>(key, id);
+    uint32_t mine = 0;                                  // lane k: round k's key, lane K: the runner-up's
     for (int k = 0; k <= a.K; ++k) {
-      uint32_t best = 0;
-#pragma unroll
-      for (int j = 0; j < NPL; ++j) best = max(best, key[j]);
-      const uint32_t win = wave_max_u32(best);
+      const uint32_t win = wave_max_u32(key[0]);
       if (win == 0) break;
-      const float v = key_value(win);
-      if (a.bias && last - v <= 2.f * tol) { near = true; break; }
-      if (k == a.K) break;
-      last = v;
-      int e = -1;
-#pragma unroll
-      for (int j = 0; j < NPL; ++j) {
-        const uint64_t holders = __ballot(key[j] == win);
-        if (e < 0 && holders) {
-          const int owner = __builtin_ctzll(holders);
-          e = MOE_WAVE * j + owner;
-          if (lane == owner) key[j] = 0;
-        }
-      }
+      const int owner = __builtin_ctzll(__ballot(key[0] == win));
+      if (lane == k) mine = win;
+      const int e = __builtin_amdgcn_readlane(id[0], owner);
       if (lane == k) my = e;
+      if (lane == owner) {
+#pragma unroll
+        for (int j = 0; j + 1 < NPL; ++j) {
+          key[j] = key[j + 1];
+          id[j] = id[j + 1];
+        }
+        key[NPL - 1] = 0;
+      }
+    }
+    if (a.bias) {
+      const uint32_t next = __shfl_down(mine, 1);
+      near = __ballot(lane < a.K && mine > 1 && next > 1 && key_value(mine) - key_value(next) <= 2.f * tol) != 0;
     }
   }
-  if (near) my = route_exact(a, row, c64, lane);
+  if (near) my = route_exact(a, row, lds + static_cast<size_t>(wave) * a.E, lane);
 
-  float w = 0.f;
-  if (lane < a.K && my >= 0) w = score(row[my]);
+  // lane k's logit, from the lane that holds it
+  float x = 0.f;
+  if constexpr (NPL <= 4) {
+    const int from = max(my, 0) / NPL;
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) {
+      const float v = __shfl(l[j], from);
+      x = max(my, 0) % NPL == j ? v : x;
+    }
+  } else {
+    x = row[max(my, 0)];
+  }
+  const bool real = lane < a.K && my >= 0;
+  float w = real ? (a.sigmoid ? sigmoid_f(x) : expf(x - m) / sum) : 0.f;
   if (a.renorm) w = w / (wave_sum_f32(w) + 1e-20f);
   if (lane < a.K) {
     a.ids[static_cast<int64_t>(t) * a.K + lane] = my;
-    a.weights[static_cast<int64_t>(t) * a.K + lane] = my >= 0 ? w * a.scale : 0.f;
+    a.weights[static_cast<int64_t>(t) * a.K + lane] = real ? w * a.scale : 0.f;
   }
 }
 
@@ -342,8 +434,9 @@ __global__ __launch_bounds__(kThreads) void group_topk_bw_kernel(RouteArgs a, co
   }
 }
 
-template <int NPL> void launch_fw(const RouteArgs& a, hipStream_t stream) {
+template <int NPL> void launch_fw(RouteArgs a, hipStream_t stream) {
   const int grid = (a.T + kWaves - 1) / kWaves;
+  a.vec = a.E % NPL == 0 && aligned16(a.logits) && aligned16(a.bias);
   group_topk_kernel<NPL><<<grid, kThreads, static_cast<size_t>(kWaves) * a.E * sizeof(double), stream>>>(a);
 }
 template <int NPL> void launch_bw(const RouteArgs& a, const float* dw, float* dl, hipStream_t stream) {
@@ -366,7 +459,7 @@ extern "C" moe_status moe_router_group_topk(const float* logits, const float* bi
   if (T == 0) return MOE_OK;
   MOE_CHECK(logits && topk_ids && topk_weights, MOE_ERR_INVALID_ARG);
   const RouteArgs a{logits, bias, T, E, K, score == MOE_SCORE_SIGMOID, n_group, topk_group, group_top, E / n_group,
-                    renorm ? 1 : 0, route_scale, topk_ids, topk_weights};
+                    renorm ? 1 : 0, route_scale, 0, topk_ids, topk_weights};
   if (E <= 64) launch_fw<1>(a, stream);
   else if (E <= 128) launch_fw<2>(a, stream);
   else if (E <= 256) launch_fw<4>(a, stream);
