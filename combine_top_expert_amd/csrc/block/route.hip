@@ -16,6 +16,8 @@
 // scores; a row in which two neighbours of the order lie within that of each
 // other is decided again by the same wave in fp64 (route_exact).
 
+#include <type_traits>
+
 #include "block_common.h"
 #include "router_common.h"
 
@@ -24,7 +26,6 @@ namespace {
 using namespace moe_block;
 using moe_router::score_key;
 using moe_router::wave_max_f32;
-using moe_router::wave_max_u32;
 using moe_router::wave_sum_f32;
 
 constexpr int kThreads = 256;
@@ -33,6 +34,21 @@ constexpr int kMaxE = 1024;
 constexpr int kMaxK = 32;
 constexpr float kMask = -3.3e38f;   // covers -inf and the lowest finite fp32 and bf16
 constexpr float kU = 5.9604644775390625e-8f;   // 2^-24, half a step of fp32
+
+// f(0), f(1), ... f(N - 1) with constant arguments: arrays indexed so stay in
+// single registers (a loop that is unrolled later makes the compiler hold
+// them as one wide register tuple, copied whole: 256 VGPRs instead of 90 for
+// sixteen scores a lane).
+template <int N, int I = 0, typename F> __device__ __forceinline__ void each(const F& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    each<N, I + 1>(f);
+  }
+}
+
+// e / size for 0 <= e < 1024, inv = 1 / size: (e + 1/2) / size is at least
+// 1 / 2048 away from every whole number, far more than its rounding.
+__device__ __forceinline__ int group_of(int e, float inv) { return static_cast<int>((static_cast<float>(e) + 0.5f) * inv); }
 
 struct RouteArgs {
   const float* logits;
@@ -48,6 +64,22 @@ struct RouteArgs {
 };
 
 __device__ __forceinline__ float sigmoid_f(float l) { return 1.0f / (1.0f + expf(-l)); }
+
+// The wave maximum of keys.  Lanes that a step does not reach read 0, the
+// maximum's identity, so that each step is one instruction (the exchange is an
+// operand modifier of the maximum).
+template <int CTRL, int ROWS = 0xF> __device__ __forceinline__ uint32_t max_step(uint32_t v) {
+  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xF, true)));
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = max_step<moe_router::kDppXor1>(v);
+  v = max_step<moe_router::kDppXor2>(v);
+  v = max_step<moe_router::kDppHalfMirror>(v);
+  v = max_step<moe_router::kDppMirror>(v);
+  v = max_step<moe_router::kDppBcast15, 0xA>(v);
+  v = max_step<moe_router::kDppBcast31, 0xC>(v);
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+}
 
 // value of a key made by score_key (keys above 1)
 __device__ __forceinline__ float key_value(uint32_t k) {
@@ -67,66 +99,108 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
   return v;
 }
 
-constexpr double kDead = -INFINITY;
-constexpr double kNan = -1e300;      // where a NaN score ranks
+// Order-preserving image of a double: every NaN is 1, below all numbers, -0 and
+// +0 map together; 0 stands for a masked or retired entry.
+__device__ __forceinline__ uint64_t key64(double v) {
+  if (v != v) return 1ull;
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+  return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double key64_value(uint64_t k) {
+  if (k <= 1ull) return k ? NAN : -INFINITY;
+  return __longlong_as_double(static_cast<int64_t>((k >> 63) ? (k ^ 0x8000000000000000ull) : ~k));
+}
+__device__ __forceinline__ uint64_t wave_max_u64(uint64_t k) {
+  const uint32_t hi = wave_max_u32(static_cast<uint32_t>(k >> 32));
+  const uint32_t lo = wave_max_u32(static_cast<uint32_t>(k >> 32) == hi ? static_cast<uint32_t>(k) : 0u);
+  return (static_cast<uint64_t>(hi) << 32) | lo;
+}
 
-// The choice in fp64: lane k returns round k's expert (or -1).  `c` is the
-// wave's LDS row of E doubles.
-__device__ __noinline__ int route_exact(const RouteArgs& a, const float* __restrict__ row, double* c, int lane) {
-  double m = kDead, sum = 0.0;
-  if (!a.sigmoid) {
-    for (int e = lane; e < a.E; e += MOE_WAVE)
-      if (!(row[e] <= kMask)) m = fmax(m, static_cast<double>(row[e]));
+// The choice in fp64: lane k returns round k's expert, or -1.  Lane l holds
+// experts l NPL + j; `lds` is the wave's row of E keys.  Rows come here seldom,
+// but a launch ends with its last wave, so this is kept short: selection on
+// registers, and every group scanned by as many lanes as there are for it.
+template <int NPL, bool SIG, bool BIAS>
+__device__ __forceinline__ int route_exact(const RouteArgs& a, const float* __restrict__ row, uint64_t* lds, int lane) {
+  const int e0 = lane * NPL;
+  float l[NPL];
+  double m = -INFINITY, sum = 0.0;
+  each<NPL>([&](auto j) {
+    l[j] = e0 + j < a.E ? row[e0 + j] : -INFINITY;
+  });
+  if (!SIG) {
+    each<NPL>([&](auto j) {
+      if (!(l[j] <= kMask)) m = fmax(m, static_cast<double>(l[j]));
+    });
     m = wave_max_f64(m);
-    for (int e = lane; e < a.E; e += MOE_WAVE)
-      if (!(row[e] <= kMask)) sum += exp(static_cast<double>(row[e]) - m);
+    each<NPL>([&](auto j) {
+      if (!(l[j] <= kMask)) sum += exp(static_cast<double>(l[j]) - m);
+      __builtin_amdgcn_sched_barrier(0);
+    });
     sum = wave_sum_f64(sum);
   }
-  for (int e = lane; e < a.E; e += MOE_WAVE) {
-    const double l = row[e];
-    double v = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - m) / sum;
-    const bool dead = row[e] <= kMask || (a.bias && a.bias[e] <= kMask);
-    if (a.bias) v += static_cast<double>(a.bias[e]);
-    c[e] = dead ? kDead : (v != v ? kNan : v);
-  }
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  uint64_t keep = ~0ull;
+  uint64_t key[NPL];
+  each<NPL>([&](auto j) {
+    key[j] = 0;
+    __builtin_amdgcn_sched_barrier(0);      // one fp64 exponential's registers at a time
+    if (l[j] <= kMask) return;
+    double v = SIG ? 1.0 / (1.0 + exp(-static_cast<double>(l[j]))) : exp(static_cast<double>(l[j]) - m) / sum;
+    if (BIAS) {
+      if (a.bias[e0 + j] <= kMask) return;
+      v += static_cast<double>(a.bias[e0 + j]);
+    }
+    key[j] = key64(v);
+  });
   if (a.n_group > 1) {
-    double gs = kDead;
-    if (lane < a.n_group) {
-      double t1 = kDead, t2 = kDead;
-      for (int i = 0; i < a.group_size; ++i) {
-        const double v = c[lane * a.group_size + i];
-        if (v > t1) { t2 = t1; t1 = v; }
-        else if (v > t2) t2 = v;
+    each<NPL>([&](auto j) {
+      if (e0 + j < a.E) lds[e0 + j] = key[j];
+    });
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const int shift = 31 - __builtin_clz(MOE_WAVE / a.n_group), P = 1 << shift;   // lanes that scan a group
+    const int g = lane >> shift;
+    uint64_t t1 = 0, t2 = 0;
+    if (g < a.n_group)
+      for (int i = lane & (P - 1); i < a.group_size; i += P) {
+        const uint64_t k = lds[g * a.group_size + i];
+        t2 = max(t2, min(t1, k));
+        t1 = max(t1, k);
       }
-      gs = (a.group_top == 2 && t2 != kDead) ? t1 + t2 : t1;
-      if (t1 == kNan || (a.group_top == 2 && t2 == kNan)) gs = kNan;
+    for (int d = 1; d < P; d <<= 1) {
+      const uint64_t o1 = __shfl_xor(t1, d), o2 = __shfl_xor(t2, d);
+      t2 = max(min(t1, o1), max(t2, o2));
+      t1 = max(t1, o1);
     }
-    keep = 0;
-    for (int g = 0; g < a.topk_group; ++g) {
-      const bool in = lane < a.n_group && !((keep >> lane) & 1);
-      const double best = wave_max_f64(in ? gs : kDead);
-      const uint64_t holders = __ballot(in && gs == best);
-      if (!holders) break;
-      keep |= holders & (~holders + 1);
+    uint64_t gk = 0;
+    if (t1) gk = (a.group_top == 2 && t2) ? key64(key64_value(t1) + key64_value(t2)) : t1;
+    int rank = 0;
+    for (int h = 0; h < a.n_group; ++h) {
+      const uint64_t o = __shfl(gk, h << shift);
+      rank += (o > gk || (o == gk && h < g)) ? 1 : 0;
     }
+    const uint64_t keep = __ballot(g < a.n_group && rank < a.topk_group);
+    const float inv = 1.0f / static_cast<float>(a.group_size);
+    each<NPL>([&](auto j) {
+      if (e0 + j < a.E && !((keep >> (group_of(e0 + j, inv) << shift)) & 1)) key[j] = 0;
+    });
   }
   int my = -1;
+#pragma unroll 1
   for (int k = 0; k < a.K; ++k) {
-    double best = kDead;
-    int be = 0x7fffffff;
-    for (int e = lane; e < a.E; e += MOE_WAVE) {
-      const double v = c[e];
-      if (v > best && ((keep >> (a.n_group > 1 ? e / a.group_size : 0)) & 1)) { best = v; be = e; }
-    }
-    const double win = wave_max_f64(best);
-    int e = (win != kDead && best == win) ? be : 0x7fffffff;
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) e = min(e, __shfl_xor(e, d));
-    if (e == 0x7fffffff) break;
-    if ((e & 63) == lane) c[e] = kDead;
+    uint64_t best = 0;
+    int be = 0;
+    each<NPL>([&](auto j) {
+      if (key[j] > best) {
+        best = key[j];
+        be = e0 + j;
+      }
+    });
+    const uint64_t win = wave_max_u64(best);
+    if (win == 0) break;
+    const int e = __builtin_amdgcn_readlane(be, __builtin_ctzll(__ballot(best == win)));
+    each<NPL>([&](auto j) {
+      if (e0 + j == e) key[j] = 0;
+    });
     if (lane == k) my = e;
   }
   return my;
@@ -135,27 +209,28 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, const float* __restr
 // exp(d) by the hardware's exp2: within (1.1 |d| + 2) kU of itself
 __device__ __forceinline__ float fast_exp(float d) { return __builtin_amdgcn_exp2f(d * 1.44269504088896341f); }
 
-// Sorts K[0..N) descending, I along with it (odd-even transposition for two,
-// else a merge network); keys of equal value keep their order.
-template <int N> __device__ __forceinline__ void sort_desc(uint32_t (&k)[N], int (&id)[N]) {
-  // stable: an exchange only where the later key is strictly larger, between
-  // neighbours; N is small and the network unrolled
-#pragma unroll
-  for (int pass = 0; pass < N; ++pass)
-#pragma unroll
-    for (int i = pass & 1; i + 1 < N; i += 2) {
-      const bool sw = k[i + 1] > k[i];
-      const uint32_t hi = max(k[i], k[i + 1]), lo = min(k[i], k[i + 1]);
-      const int a = sw ? id[i + 1] : id[i], b = sw ? id[i] : id[i + 1];
-      k[i] = hi; k[i + 1] = lo;
-      id[i] = a; id[i + 1] = b;
+// Sorts k descending, id along with it, by N passes of exchanges between
+// neighbours where the later key is strictly larger: equal keys keep their
+// order.  (Recursion, so that every index is a constant.)
+template <int PASS, int I, int N> __device__ __forceinline__ void stable_sort(uint32_t (&k)[N], int (&id)[N]) {
+  if constexpr (PASS < N) {
+    if constexpr (I + 1 < N) {
+      const bool sw = k[I + 1] > k[I];
+      const uint32_t hi = max(k[I], k[I + 1]), lo = min(k[I], k[I + 1]);
+      const int a = sw ? id[I + 1] : id[I], b = sw ? id[I] : id[I + 1];
+      k[I] = hi; k[I + 1] = lo;
+      id[I] = a; id[I + 1] = b;
+      stable_sort<PASS, I + 2>(k, id);
+    } else {
+      stable_sort<PASS + 1, (PASS + 1) & 1>(k, id);
     }
+  }
 }
 
 // (t1, t2) <- the two largest of this lane's and its partner's
 template <int CTRL> __device__ __forceinline__ void merge2(uint32_t& t1, uint32_t& t2) {
-  const uint32_t o1 = moe_router::dpp_u32<CTRL>(t1, t1), o2 = moe_router::dpp_u32<CTRL>(t2, t2);
-  t2 = max(min(t1, o1), max(t2, o2));
+  const uint32_t o1 = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(t1), CTRL, 0xF, 0xF, true));
+  t2 = max(min(t1, o1), max_step<CTRL>(t2));
   t1 = max(t1, o1);
 }
 __device__ __forceinline__ void merge2_shfl(uint32_t& t1, uint32_t& t2, int d) {
@@ -164,9 +239,9 @@ __device__ __forceinline__ void merge2_shfl(uint32_t& t1, uint32_t& t2, int d) {
   t1 = max(t1, o1);
 }
 
-template <int NPL>   // scores per lane: E <= 64 * NPL
+template <int NPL, bool SIG, bool BIAS>   // scores per lane: E <= 64 * NPL
 __global__ __launch_bounds__(kThreads) void group_topk_kernel(RouteArgs a) {
-  extern __shared__ double lds[];
+  extern __shared__ uint64_t lds[];
   const int lane = moe::lane_id();
   const int wave = threadIdx.x >> 6;
   const int t = blockIdx.x * kWaves + wave;
@@ -183,7 +258,7 @@ __global__ __launch_bounds__(kThreads) void group_topk_kernel(RouteArgs a) {
       vec_t v = {}, w = {};
       if (e0 < a.E) {
         v = *reinterpret_cast<const vec_t*>(row + e0 + j);
-        if (a.bias) w = *reinterpret_cast<const vec_t*>(a.bias + e0 + j);
+        if (BIAS) w = *reinterpret_cast<const vec_t*>(a.bias + e0 + j);
       }
 #pragma unroll
       for (int i = 0; i < W; ++i) {
@@ -192,71 +267,71 @@ __global__ __launch_bounds__(kThreads) void group_topk_kernel(RouteArgs a) {
       }
     }
   } else {
-#pragma unroll
-    for (int j = 0; j < NPL; ++j) {
+    each<NPL>([&](auto j) {
       l[j] = e0 + j < a.E ? row[e0 + j] : -INFINITY;
-      b[j] = a.bias && e0 + j < a.E ? a.bias[e0 + j] : 0.f;
-    }
+      b[j] = BIAS && e0 + j < a.E ? a.bias[e0 + j] : 0.f;
+    });
   }
 
   float m = 0.f, sum = 1.f, inv = 1.f;
-  if (!a.sigmoid) {
+  if (!SIG) {
     m = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < NPL; ++j)
+    each<NPL>([&](auto j) {
       if (!(l[j] <= kMask)) m = fmaxf(m, l[j]);
+    });
     m = wave_max_f32(m);
     sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < NPL; ++j)
+    each<NPL>([&](auto j) {
       if (!(l[j] <= kMask)) sum += fast_exp(l[j] - m);
+    });
     sum = wave_sum_f32(sum);
     inv = 1.0f / sum;
   }
   auto fast_score = [&](float x) {
-    return a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-x)) : fast_exp(x - m) * inv;
+    return SIG ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-x)) : fast_exp(x - m) * inv;
   };
 
   // Keys: of the logits without a bias, of c with one.  fast_score is off by at
   // most (1.1 |d| + 2 + 1 + 2) kU of itself (d: the exponent; exp, add and
   // reciprocal), for softmax by the sum's and the quotient's roundings too
   // (NPL + 6 additions, terms that are off by 5 kU on average at most).
-  const float c0 = a.sigmoid ? 6.f : 20.f + NPL;
+  const float c0 = SIG ? 6.f : 20.f + NPL;
   uint32_t key[NPL];
   int id[NPL];
-  float err = 0.f;
-#pragma unroll
-  for (int j = 0; j < NPL; ++j) {
-    key[j] = 0;
+  float err = 0.f, all = 0.f;
+  each<NPL>([&](auto j) {
     id[j] = e0 + j;
-    const bool live = !(l[j] <= kMask);
-    if (a.bias) {
+    asm("" : "+v"(id[j]));            // a value to move along, not an index to select by
+    if (BIAS) {
+      // plain order-preserving image: -0 below +0 and NaN anywhere, but equal
+      // scores and NaN are decided in fp64 below
       const float s = fast_score(l[j]), v = s + b[j];
-      if (live && !(b[j] <= kMask)) {
-        key[j] = max(score_key(v), 1u);
-        const float d = a.sigmoid ? l[j] : l[j] - m;
-        err = fmaxf(err, fmaf(s, fmaf(1.5f, fabsf(d), c0), fabsf(v) < INFINITY ? fabsf(v) : 0.f));
-      }
-    } else if (live) {
-      key[j] = sum != sum ? 1u : max(score_key(l[j]), 1u);
+      const uint32_t u = __float_as_uint(v);
+      const uint32_t k = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+      const bool live = !(l[j] <= kMask) && !(b[j] <= kMask);
+      const float d = SIG ? l[j] : l[j] - m;
+      key[j] = live ? k : 0u;
+      err = fmaxf(err, live ? fmaf(s, fmaf(1.5f, fabsf(d), c0), fabsf(v)) : 0.f);
+      all += live ? v : 0.f;
+    } else {
+      key[j] = l[j] <= kMask ? 0u : (sum != sum ? 1u : max(score_key(l[j]), 1u));
     }
-  }
+  });
   // how far a c may be off: 0 without a bias, where keys are exact
-  const float tol = a.bias ? wave_max_f32(err) * kU : 0.f;
+  const float tol = BIAS ? wave_max_f32(err) * kU : 0.f;
 
-  bool near = false;
-  if (a.n_group > 1) {
+  bool near = BIAS && __ballot(all != all) != 0;       // a NaN among the scores
+  if (a.n_group > 1 && !near) {
     const int gs = a.group_size;
     const int lg = gs / NPL;                            // lanes of a group
     const bool runs = gs % NPL == 0 && (lg & (lg - 1)) == 0;
     uint32_t t1 = 0, t2 = 0;
     int g, stride;                                      // this lane's group, lanes between groups
     if (runs) {
-#pragma unroll
-      for (int j = 0; j < NPL; ++j) {
+      each<NPL>([&](auto j) {
         t2 = max(t2, min(t1, key[j]));
         t1 = max(t1, key[j]);
-      }
+      });
       if (lg >= 2) merge2<moe_router::kDppXor1>(t1, t2);
       if (lg >= 4) merge2<moe_router::kDppXor2>(t1, t2);
       if (lg >= 8) merge2<moe_router::kDppHalfMirror>(t1, t2);
@@ -267,9 +342,9 @@ __global__ __launch_bounds__(kThreads) void group_topk_kernel(RouteArgs a) {
       stride = lg;
     } else {
       uint32_t* c32 = reinterpret_cast<uint32_t*>(lds + static_cast<size_t>(wave) * a.E);
-#pragma unroll
-      for (int j = 0; j < NPL; ++j)
+      each<NPL>([&](auto j) {
         if (e0 + j < a.E) c32[e0 + j] = key[j];
+      });
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
       if (lane < a.n_group)
@@ -286,82 +361,82 @@ __global__ __launch_bounds__(kThreads) void group_topk_kernel(RouteArgs a) {
     if (t1 && g < a.n_group) {
       float v = key_value(t1);
       if (a.group_top == 2) {
-        if (!a.bias) v = fast_score(v);
-        if (t2) v += a.bias ? key_value(t2) : fast_score(key_value(t2));
+        if (!BIAS) v = fast_score(v);
+        if (t2) v += BIAS ? key_value(t2) : fast_score(key_value(t2));
       }
       gkey = max(score_key(v), 1u);
     }
     int rank = 0;
     for (int h = 0; h < a.n_group; ++h) {
+      // o > gkey, or o == gkey from a lower group
       const uint32_t o = __builtin_amdgcn_readlane(gkey, h * stride);
-      rank += (o > gkey || (o == gkey && h < g)) ? 1 : 0;
+      rank += o + (h < g ? 1u : 0u) > gkey ? 1 : 0;
     }
     const bool kept = g < a.n_group && rank < a.topk_group;
     // the last group that stays and the first that does not
     const uint64_t in = __ballot(g < a.n_group && rank == a.topk_group - 1);
     const uint64_t out = __ballot(g < a.n_group && rank == a.topk_group);
-    if (out && (a.bias || a.group_top == 2)) {
+    if (out && (BIAS || a.group_top == 2)) {
       const uint32_t ki = __builtin_amdgcn_readlane(gkey, __builtin_ctzll(in));
       const uint32_t ko = __builtin_amdgcn_readlane(gkey, __builtin_ctzll(out));
       if (ki > 1 && ko > 1) {
         const float vi = key_value(ki), vo = key_value(ko);
         // without a bias a sum of two scores is off by its own share
         // (exponents to 88) and by what fp32 loses below its normal range
-        near = vi - vo <= (a.bias ? 4.f * tol + 2.f * kU * (fabsf(vi) + fabsf(vo)) : (c0 + 140.f) * kU * (vi + vo) + 1e-37f);
+        near = vi - vo <= (BIAS ? 4.f * tol + 2.f * kU * (fabsf(vi) + fabsf(vo)) : (c0 + 140.f) * kU * (vi + vo) + 1e-37f);
       }
     }
     if (runs) {
-#pragma unroll
-      for (int j = 0; j < NPL; ++j) key[j] = kept ? key[j] : 0u;
+      each<NPL>([&](auto j) {
+        key[j] = kept ? key[j] : 0u;
+      });
     } else {
       const uint64_t keep = __ballot(kept);
-#pragma unroll
-      for (int j = 0; j < NPL; ++j)
-        if (e0 + j < a.E && !((keep >> ((e0 + j) / gs)) & 1)) key[j] = 0;
+      each<NPL>([&](auto j) {
+        if (e0 + j < a.E && !((keep >> group_of(e0 + j, 1.0f / static_cast<float>(gs))) & 1)) key[j] = 0;
+      });
     }
   }
 
   int my = -1;
   if (!near) {
-    sort_desc<NPL>(key, id);
+    stable_sort<0, 0>(key, id);
     uint32_t mine = 0;                                  // lane k: round k's key, lane K: the runner-up's
     for (int k = 0; k <= a.K; ++k) {
       const uint32_t win = wave_max_u32(key[0]);
       if (win == 0) break;
       const int owner = __builtin_ctzll(__ballot(key[0] == win));
-      if (lane == k) mine = win;
       const int e = __builtin_amdgcn_readlane(id[0], owner);
-      if (lane == k) my = e;
+      mine = lane == k ? win : mine;
+      my = lane == k ? e : my;
       if (lane == owner) {
-#pragma unroll
-        for (int j = 0; j + 1 < NPL; ++j) {
+        each<NPL - 1>([&](auto j) {
           key[j] = key[j + 1];
           id[j] = id[j + 1];
-        }
+        });
         key[NPL - 1] = 0;
       }
     }
-    if (a.bias) {
+    if (BIAS) {
       const uint32_t next = __shfl_down(mine, 1);
       near = __ballot(lane < a.K && mine > 1 && next > 1 && key_value(mine) - key_value(next) <= 2.f * tol) != 0;
     }
   }
-  if (near) my = route_exact(a, row, lds + static_cast<size_t>(wave) * a.E, lane);
+  if (near) my = route_exact<NPL, SIG, BIAS>(a, row, lds + static_cast<size_t>(wave) * a.E, lane);
 
   // lane k's logit, from the lane that holds it
   float x = 0.f;
   if constexpr (NPL <= 4) {
     const int from = max(my, 0) / NPL;
-#pragma unroll
-    for (int j = 0; j < NPL; ++j) {
+    each<NPL>([&](auto j) {
       const float v = __shfl(l[j], from);
       x = max(my, 0) % NPL == j ? v : x;
-    }
+    });
   } else {
     x = row[max(my, 0)];
   }
   const bool real = lane < a.K && my >= 0;
-  float w = real ? (a.sigmoid ? sigmoid_f(x) : expf(x - m) / sum) : 0.f;
+  float w = real ? (SIG ? sigmoid_f(x) : expf(x - m) / sum) : 0.f;
   if (a.renorm) w = w / (wave_sum_f32(w) + 1e-20f);
   if (lane < a.K) {
     a.ids[static_cast<int64_t>(t) * a.K + lane] = my;
@@ -369,9 +444,200 @@ __global__ __launch_bounds__(kThreads) void group_topk_kernel(RouteArgs a) {
   }
 }
 
+// Four tokens per wave, one per 16-lane row of lanes, for large batches with a
+// bias: everything stays in the row (a row maximum is four DPP steps and all
+// lanes have it), and one instruction works for four tokens.  A lane holds NPL
+// (8 or 16) neighbouring experts.
+//
+// Keys are the order-preserving images of c with the four lowest bits replaced
+// by 15 - j, j the expert's place in its lane, so that sorting moves one
+// register per expert; what the truncation hides (32 kU of c) is added to the
+// distance below which a row is decided in fp64.  At most kSegK experts are
+// taken, so a lane's list is kept to its kSegK + 1 largest.
+constexpr int kSeg = 16;
+constexpr int kSegK = 8;
+
+// Sorts k[LO .. LO + N) descending by Batcher's odd-even merges (63 exchanges
+// of 16 keys).
+template <int A, int B, int M> __device__ __forceinline__ void exchange(uint32_t (&k)[M]) {
+  const uint32_t hi = max(k[A], k[B]);
+  k[B] = min(k[A], k[B]);
+  k[A] = hi;
+}
+template <int LO, int N, int R, int I, int M> __device__ __forceinline__ void merge_odd(uint32_t (&k)[M]) {
+  if constexpr (I + R < LO + N) {
+    exchange<I, I + R>(k);
+    merge_odd<LO, N, R, I + 2 * R>(k);
+  }
+}
+template <int LO, int N, int R, int M> __device__ __forceinline__ void merge_sorted(uint32_t (&k)[M]) {
+  if constexpr (2 * R < N) {
+    merge_sorted<LO, N, 2 * R>(k);
+    merge_sorted<LO + R, N, 2 * R>(k);
+    merge_odd<LO, N, R, LO + R>(k);
+  } else {
+    exchange<LO, LO + R>(k);
+  }
+}
+template <int LO, int N, int M> __device__ __forceinline__ void merge_sort_desc(uint32_t (&k)[M]) {
+  if constexpr (N > 1) {
+    merge_sort_desc<LO, N / 2>(k);
+    merge_sort_desc<LO + N / 2, N / 2>(k);
+    merge_sorted<LO, N, 1>(k);
+  }
+}
+
+// the lowest set bit of each 16-bit field
+__device__ __forceinline__ uint64_t lowest_of_rows(uint64_t m) {
+  constexpr uint64_t top = 0x8000800080008000ull, one = 0x0001000100010001ull;
+  const uint64_t n = ~m;
+  return m & (((n & ~top) + one) ^ (n & top));          // m & -m, field by field
+}
+
+template <int CTRL> __device__ __forceinline__ void merge2f(float& t1, float& t2) {
+  const float o1 = moe_router::dpp_f32<CTRL>(t1, t1), o2 = moe_router::dpp_f32<CTRL>(t2, t2);
+  t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
+  t1 = fmaxf(t1, o1);
+}
+
+template <int NPL, bool SIG>
+__global__ __launch_bounds__(kThreads) void group_topk_seg_kernel(RouteArgs a) {
+  extern __shared__ uint64_t lds[];
+  __shared__ uint2 ring[kWaves][MOE_WAVE / kSeg][kSegK + 1];
+  const int lane = moe::lane_id();
+  const int wave = threadIdx.x >> 6;
+  const int sl = lane & (kSeg - 1), seg = lane / kSeg;
+  const int t0 = (blockIdx.x * kWaves + wave) * (MOE_WAVE / kSeg);
+  if (t0 >= a.T) return;
+  const int t = min(t0 + seg, a.T - 1);                 // a row past the end repeats the last, unstored
+  const float* row = a.logits + static_cast<int64_t>(t) * a.E;
+  const int e0 = sl * NPL;
+  const bool used = e0 < a.E;
+
+  float l[NPL], c[NPL];
+#pragma unroll
+  for (int j = 0; j < NPL; j += 4) {
+    float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY), w = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (used) {
+      v = *reinterpret_cast<const float4*>(row + e0 + j);
+      w = *reinterpret_cast<const float4*>(a.bias + e0 + j);
+    }
+    l[j] = v.x; l[j + 1] = v.y; l[j + 2] = v.z; l[j + 3] = v.w;
+    c[j] = w.x; c[j + 1] = w.y; c[j + 2] = w.z; c[j + 3] = w.w;
+  }
+  float lmax = -INFINITY;
+  each<NPL>([&](auto j) {
+    lmax = fmaxf(lmax, l[j]);
+  });
+  lmax = moe_router::row_max_f32(lmax);
+  float sum = 1.f, inv = 1.f;
+  if (!SIG) {
+    sum = 0.f;
+    each<NPL>([&](auto j) {
+      sum += l[j] <= kMask ? 0.f : fast_exp(l[j] - lmax);
+    });
+    sum = moe_router::row_sum_f32(sum);
+    inv = 1.0f / sum;
+  }
+  // c, and the rows whose scores are no ordinary numbers
+  uint64_t odd = 0;
+  each<NPL>([&](auto j) {
+    const float s = SIG ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-l[j])) : fast_exp(l[j] - lmax) * inv;
+    c[j] = l[j] <= kMask ? -INFINITY : s + c[j];
+    odd |= __ballot(!(c[j] < INFINITY));
+  });
+  bool near = ((odd >> (seg * kSeg)) & 0xffffu) != 0;
+  // How far a c may be off, its own rounding aside: fast_exp's share of s grows
+  // with the exponent, but s |l| is at most smax |lmax| + 1.3 smax (sigmoid), and
+  // exp(-d) d at most 0.37 (softmax, plus the sum's NPL + 4 additions).
+  const float smax = SIG ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-lmax)) : inv;
+  const float tol = smax * (SIG ? 8.f + 1.5f * fabsf(lmax) : 20.f + NPL) * kU;
+
+  bool kept = true;
+  if (a.n_group > 1) {
+    const int lg = a.group_size / NPL;                  // lanes of a group, a power of two
+    float t1 = -INFINITY, t2 = -INFINITY;
+    each<NPL>([&](auto j) {
+      t2 = __builtin_amdgcn_fmed3f(t1, t2, c[j]);
+      t1 = fmaxf(t1, c[j]);
+    });
+    if (lg >= 2) merge2f<moe_router::kDppXor1>(t1, t2);
+    if (lg >= 4) merge2f<moe_router::kDppXor2>(t1, t2);
+    if (lg >= 8) merge2f<moe_router::kDppHalfMirror>(t1, t2);
+    if (lg >= 16) merge2f<moe_router::kDppMirror>(t1, t2);
+    const bool dead = !(t1 > kMask);
+    const float gs = dead ? -INFINITY : (a.group_top == 2 && t2 > kMask) ? t1 + t2 : t1;
+    int rank = 0;
+    for (int h = 0; h < a.n_group; ++h) rank += __shfl(gs, h * lg, kSeg) > gs ? 1 : 0;
+    kept = !dead && rank < a.topk_group;
+    // the worst group that stays against the best that does not; equal scores
+    // share a rank, so a tie at the edge keeps too many
+    const float vi = -moe_router::row_max_f32(kept ? -gs : -INFINITY);
+    const float vo = moe_router::row_max_f32(kept ? -INFINITY : gs);
+    const uint32_t lanes = static_cast<uint32_t>(__ballot(kept && used) >> (seg * kSeg)) & 0xffffu;
+    near |= vi - vo <= 4.f * tol + 4.f * kU * (fabsf(vi) + fabsf(vo)) || __popc(lanes) > a.topk_group * lg;
+  }
+
+  uint32_t key[NPL];
+  each<NPL>([&](auto j) {
+    const uint32_t u = __float_as_uint(c[j]);
+    const uint32_t k = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+    key[j] = ((kept && c[j] > kMask ? k : 0u) & ~15u) | (15u - j);
+  });
+  merge_sort_desc<0, NPL>(key);
+  constexpr int kKeep = NPL < kSegK + 1 ? NPL : kSegK + 1;
+  for (int k = 0; k <= a.K; ++k) {
+    uint32_t win = max_step<moe_router::kDppXor1>(key[0]);
+    win = max_step<moe_router::kDppXor2>(win);
+    win = max_step<moe_router::kDppHalfMirror>(win);
+    win = max_step<moe_router::kDppMirror>(win);
+    const uint64_t owners = lowest_of_rows(__ballot(key[0] == win));
+    if ((owners >> lane) & 1) {
+      ring[wave][seg][k] = make_uint2(win, e0 + 15 - (win & 15u));
+      each<kKeep - 1>([&](auto j) {
+        key[j] = key[j + 1];
+      });
+      key[kKeep - 1] = 0;
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+
+  int my = -1;
+  if (sl < a.K) {
+    const uint2 w = ring[wave][seg][sl], next = ring[wave][seg][sl + 1];
+    if (w.x > 15u) {
+      my = static_cast<int>(w.y);
+      const float v = key_value(w.x & ~15u), o = key_value(next.x & ~15u);
+      near |= next.x > 15u && v - o <= 2.f * tol + 40.f * kU * fmaxf(fabsf(v), fabsf(o));
+    }
+  }
+  // the tokens that are decided in fp64, one after the other by the whole wave
+  const uint64_t again = __ballot(near);
+#pragma unroll 1
+  for (int g = 0; g < MOE_WAVE / kSeg; ++g) {
+    if (((again >> (g * kSeg)) & 0xffffu) == 0 || t0 + g >= a.T) continue;
+    const int id = route_exact<NPL / 4, SIG, true>(a, a.logits + static_cast<int64_t>(t0 + g) * a.E,
+                                          lds + static_cast<size_t>(wave) * a.E, lane);
+    const int moved = __shfl(id, sl);
+    if (seg == g) my = sl < a.K ? moved : -1;
+  }
+
+  float w = 0.f;
+  if (my >= 0) {
+    const float x = row[my];
+    w = SIG ? sigmoid_f(x) : expf(x - lmax) / sum;
+  }
+  if (a.renorm) w = w / (moe_router::row_sum_f32(w) + 1e-20f);
+  if (sl < a.K && t0 + seg < a.T) {
+    a.ids[static_cast<int64_t>(t) * a.K + sl] = my;
+    a.weights[static_cast<int64_t>(t) * a.K + sl] = my >= 0 ? w * a.scale : 0.f;
+  }
+}
+
 // Backward: one wavefront per token.  Lane k holds route k's id, score and
 // ds; the row's other elements are 0 (sigmoid) or the softmax's -s_e dot.
-template <int NPL>
+template <int NPL, bool SIG>
 __global__ __launch_bounds__(kThreads) void group_topk_bw_kernel(RouteArgs a, const float* __restrict__ d_weights,
                                                                  float* __restrict__ d_logits) {
   const int lane = moe::lane_id();
@@ -380,32 +646,31 @@ __global__ __launch_bounds__(kThreads) void group_topk_bw_kernel(RouteArgs a, co
   const float* row = a.logits + static_cast<int64_t>(t) * a.E;
   float l[NPL];
   float m = 0.f, sum = 1.f;
-  if (!a.sigmoid) {
+  if (!SIG) {
     m = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < NPL; ++j) {
+    each<NPL>([&](auto j) {
       const int e = lane + MOE_WAVE * j;
       l[j] = e < a.E ? row[e] : -INFINITY;
       if (!(l[j] <= kMask)) m = fmaxf(m, l[j]);
-    }
+    });
     m = wave_max_f32(m);
     sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < NPL; ++j) {
+    each<NPL>([&](auto j) {
       l[j] = l[j] <= kMask ? 0.f : expf(l[j] - m);
       sum += l[j];
-    }
+    });
     sum = wave_sum_f32(sum);
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-#pragma unroll
-    for (int j = 0; j < NPL; ++j) l[j] *= inv;      // s
+    each<NPL>([&](auto j) {
+      l[j] *= inv;
+    });      // s
   }
   int id = lane < a.K ? a.ids[static_cast<int64_t>(t) * a.K + lane] : -1;
   if (id >= a.E) id = -1;
   float s = 0.f, d = 0.f;
   if (id >= 0) {
     const float x = row[id];
-    if (!(x <= kMask)) s = a.sigmoid ? sigmoid_f(x) : expf(x - m) / sum;
+    if (!(x <= kMask)) s = SIG ? sigmoid_f(x) : expf(x - m) / sum;
     d = d_weights[static_cast<int64_t>(t) * a.K + lane] * a.scale;
   }
   if (a.renorm) {
@@ -414,33 +679,57 @@ __global__ __launch_bounds__(kThreads) void group_topk_bw_kernel(RouteArgs a, co
     d = id >= 0 ? (d - dot) / S : 0.f;
   }
   // g: what route k adds to its expert's element
-  const float dot = a.sigmoid ? 0.f : wave_sum_f32(d * s);
-  const float g = a.sigmoid ? d * s * (1.0f - s) : d * s;
+  const float dot = SIG ? 0.f : wave_sum_f32(d * s);
+  const float g = SIG ? d * s * (1.0f - s) : d * s;
   float o[NPL];
-#pragma unroll
-  for (int j = 0; j < NPL; ++j) o[j] = a.sigmoid ? 0.f : -l[j] * dot;
+  each<NPL>([&](auto j) {
+    o[j] = SIG ? 0.f : -l[j] * dot;
+  });
   for (int k = 0; k < a.K; ++k) {
     const int e = __builtin_amdgcn_readlane(id, k);
     if (e < 0) continue;
     const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g), k));
-#pragma unroll
-    for (int j = 0; j < NPL; ++j)
+    each<NPL>([&](auto j) {
       if (e == lane + MOE_WAVE * j) o[j] += v;
+    });
   }
-#pragma unroll
-  for (int j = 0; j < NPL; ++j) {
+  each<NPL>([&](auto j) {
     const int e = lane + MOE_WAVE * j;
     if (e < a.E) d_logits[static_cast<int64_t>(t) * a.E + e] = o[j];
-  }
+  });
+}
+
+template <int NPL> void launch_seg(const RouteArgs& a, hipStream_t stream) {
+  constexpr int kTok = kWaves * (MOE_WAVE / kSeg);
+  const int grid = (a.T + kTok - 1) / kTok;
+  const size_t shared = static_cast<size_t>(kWaves) * a.E * sizeof(uint64_t);
+  if (a.sigmoid) group_topk_seg_kernel<NPL, true><<<grid, kThreads, shared, stream>>>(a);
+  else group_topk_seg_kernel<NPL, false><<<grid, kThreads, shared, stream>>>(a);
+}
+
+// Whether the four-tokens-a-wave kernel takes this call.
+template <int NPL> bool seg_fits(const RouteArgs& a) {
+  const int lg = a.group_size / NPL;
+  return a.bias && a.K <= kSegK && a.E % NPL == 0 && aligned16(a.logits) && aligned16(a.bias) &&
+         (a.n_group == 1 || (a.group_size % NPL == 0 && (lg & (lg - 1)) == 0));
 }
 
 template <int NPL> void launch_fw(RouteArgs a, hipStream_t stream) {
   const int grid = (a.T + kWaves - 1) / kWaves;
   a.vec = a.E % NPL == 0 && aligned16(a.logits) && aligned16(a.bias);
-  group_topk_kernel<NPL><<<grid, kThreads, static_cast<size_t>(kWaves) * a.E * sizeof(double), stream>>>(a);
+  const size_t shared = static_cast<size_t>(kWaves) * a.E * sizeof(uint64_t);
+  if (a.sigmoid) {
+    if (a.bias) group_topk_kernel<NPL, true, true><<<grid, kThreads, shared, stream>>>(a);
+    else group_topk_kernel<NPL, true, false><<<grid, kThreads, shared, stream>>>(a);
+  } else {
+    if (a.bias) group_topk_kernel<NPL, false, true><<<grid, kThreads, shared, stream>>>(a);
+    else group_topk_kernel<NPL, false, false><<<grid, kThreads, shared, stream>>>(a);
+  }
 }
 template <int NPL> void launch_bw(const RouteArgs& a, const float* dw, float* dl, hipStream_t stream) {
-  group_topk_bw_kernel<NPL><<<(a.T + kWaves - 1) / kWaves, kThreads, 0, stream>>>(a, dw, dl);
+  const int grid = (a.T + kWaves - 1) / kWaves;
+  if (a.sigmoid) group_topk_bw_kernel<NPL, true><<<grid, kThreads, 0, stream>>>(a, dw, dl);
+  else group_topk_bw_kernel<NPL, false><<<grid, kThreads, 0, stream>>>(a, dw, dl);
 }
 
 }  // namespace
@@ -460,7 +749,14 @@ extern "C" moe_status moe_router_group_topk(const float* logits, const float* bi
   MOE_CHECK(logits && topk_ids && topk_weights, MOE_ERR_INVALID_ARG);
   const RouteArgs a{logits, bias, T, E, K, score == MOE_SCORE_SIGMOID, n_group, topk_group, group_top, E / n_group,
                     renorm ? 1 : 0, route_scale, 0, topk_ids, topk_weights};
-  if (E <= 64) launch_fw<1>(a, stream);
+  // Four tokens a wave from 5120 tokens on, where they fill the card: wave per
+  // token against four tokens a wave, us, E = 256, K = 8, 4 of 8 groups: 128
+  // tokens 4.5 / 5.9, 2048: 8.5 / 9.4, 4096: 9.6 / 9.5, 8192: 13.7 / 12.0, 65536:
+  // 58 / 32; E = 128, K = 6: 4096: 6.6 / 6.9, 8192: 8.9 / 7.6, 65536: 41 / 20.
+  constexpr int kSegFrom = 5120;
+  if (T >= kSegFrom && E > 128 && E <= 256 && seg_fits<16>(a)) launch_seg<16>(a, stream);
+  else if (T >= kSegFrom && E > 64 && E <= 128 && seg_fits<8>(a)) launch_seg<8>(a, stream);
+  else if (E <= 64) launch_fw<1>(a, stream);
   else if (E <= 128) launch_fw<2>(a, stream);
   else if (E <= 256) launch_fw<4>(a, stream);
   else if (E <= 512) launch_fw<8>(a, stream);

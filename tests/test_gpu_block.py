@@ -307,6 +307,37 @@ def test_route_many_tokens(ep, T):
     inside(w[some], rw, 64 * U * rw, "weights")
 
 
+@pytest.mark.parametrize("E,K,n,keep", [(256, 8, 8, 4), (256, 8, 1, 1), (256, 1, 16, 1), (160, 6, 5, 2), (160, 6, 1, 1), (128, 6, 4, 2),
+                                        (96, 3, 3, 2), (128, 8, 16, 9), (192, 8, 4, 2)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_large_batches(ep, E, K, n, keep, score):
+    """5123 tokens and more go four to a wave: ordinary rows, masked ones, ties
+    and near ties, NaN and infinities, in every place of a wave; the choice is
+    that of the oracle, and the tail of the last wave stays unwritten."""
+    announce("route large", E, K, n, keep, score)
+    rng = np.random.default_rng(E + K + n)
+    rows = [1.5 * rng.standard_normal((9, E)), np.round(rng.standard_normal((6, E)) * 2) / 2,
+            0.5 + 3e-7 * rng.integers(-3, 4, (6, E)), np.full((1, E), -np.inf), np.zeros((1, E)),
+            np.where(rng.random((8, E)) < np.linspace(0.1, 0.99, 8)[:, None], -np.inf, rng.standard_normal((8, E))),
+            -30 + 5 * rng.standard_normal((2, E)), 20 + 5 * rng.standard_normal((2, E))]
+    x = np.concatenate(rows).astype(np.float32)
+    x = np.concatenate([x, x[:4]])
+    x[-4, 3], x[-3, 5], x[-2, 1] = np.nan, 90.0, -np.finfo(np.float32).max
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
+    masked = np.where(rng.random(E) < 0.3, -np.inf, bias).astype(np.float32)
+    T = 5123
+    big = np.resize(np.arange(len(x)), T)
+    for b in (bias, masked, (np.round(bias * 8) / 8).astype(np.float32)):
+        for top in (1, 2):
+            rid, rw = ob.group_topk(x, K, b, score, n, keep, top, True, 2.0)
+            ids, w = route(ep, x[big], K, b, score, n, keep, top, True, 2.0)
+            assert np.array_equal(ids, rid[big]), np.argwhere(ids != rid[big])[:4].tolist()
+            ok = np.isfinite(rw).all(axis=1)[big]
+            assert np.isnan(w[~ok]).any(axis=1).all()
+            # softmax: a chosen score's exponent, at most 60 here, and the sum's
+            inside(w[ok], rw[big][ok], (64 + (120 if score == "softmax" else 0)) * U * np.abs(rw[big][ok]) + 1e-30, "weights")
+
+
 @pytest.mark.parametrize("E,K", [(8, 1), (16, 16), (64, 6), (100, 7), (256, 8), (1000, 16), (1024, 32)])
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 def test_route_backward(ep, E, K, score):
