@@ -4,9 +4,9 @@
 // r = 1 / sqrt(mean h^2 + eps), written as bf16/fp32 rows and/or block FP8.
 // Backward: dx = dh + r (w dy - n mean(w dy n)), n = h r; d_w = sum_t dy n.
 //
-// A group of WAVES wavefronts owns a row and holds it in registers as chunks
-// of 8 neighbouring columns (chunk c of lane i: 8 (64 WAVES v + i)), so a row
-// is read once and every access is 16 bytes per lane.  Sums run in fp32: per
+// A block owns a row and holds it in registers as chunks of 8 neighbouring
+// columns (chunk v of thread i: columns 8 (threads v + i)), so a row is read
+// once and every access is 16 bytes per lane.  Sums run in fp32: per
 // lane, a DPP wave sum, then the waves' sums through LDS in wave order.  A
 // group of 128 columns is 16 neighbouring lanes, whose amax is an in-row DPP
 // maximum.
@@ -19,56 +19,119 @@ namespace {
 using namespace moe_block;
 
 constexpr int kMaxH = 16384;
+constexpr int kMaxWaves = 16;
 
-// Sum over the WAVES waves of the block; every thread gets it.  `red` has
-// WAVES entries; the leading barrier covers reads of an earlier call's values.
-template <int WAVES> __device__ __forceinline__ float block_sum(float v, float* red) {
+// Sums over the block's waves of two values; every thread gets them, added in
+// wave order.  `red` must not be the array of the call before (one barrier
+// orders the writes before the reads, and only that).
+__device__ __forceinline__ float2 block_sum(float u, float v, int waves, float2* red) {
+  u = moe_router::wave_sum_f32(u);
   v = moe_router::wave_sum_f32(v);
-  if constexpr (WAVES == 1) return v;
+  if (waves == 1) return make_float2(u, v);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = make_float2(u, v);
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = red[0];
-#pragma unroll
-  for (int i = 1; i < WAVES; ++i) s += red[i];
+  float2 s = red[0];
+  for (int i = 1; i < waves; ++i) {
+    s.x += red[i].x;
+    s.y += red[i].y;
+  }
   return s;
 }
 
-template <typename T, typename TW, int WAVES, int VPL>
-__global__ __launch_bounds__(WAVES * 64) void add_rms_norm_kernel(const T* x, const T* residual,
-                                                                 const TW* __restrict__ weight, float eps, int H,
-                                                                 T* h_out, T* y, uint8_t* __restrict__ y8,
-                                                                 float* __restrict__ scales) {
-  __shared__ float red[WAVES];
+// 16 bytes, with NT past the caches' retention: from 32 MB of rows on, what a
+// call reads and writes does not stay in the 32 MB of L2 in any case
+// (measured below).
+template <bool NT> __device__ __forceinline__ uint4 get16(const void* p) {
+  return NT ? moe::load_nt16(p) : *reinterpret_cast<const uint4*>(p);
+}
+template <bool NT> __device__ __forceinline__ void put16(void* p, const uint4& v) {
+  if (NT) moe::store_nt16(p, v);
+  else *reinterpret_cast<uint4*>(p) = v;
+}
+
+// Eight neighbouring elements as loaded.
+template <typename T> struct Chunk;
+template <> struct Chunk<float> {
+  uint4 a, b;
+  template <bool NT> __device__ __forceinline__ void load(const float* p) {
+    a = get16<NT>(p);
+    b = get16<NT>(p + 4);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y); f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
+    f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y); f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+  }
+};
+template <> struct Chunk<uint16_t> {
+  uint4 a;
+  template <bool NT> __device__ __forceinline__ void load(const uint16_t* p) { a = get16<NT>(p); }
+  __device__ __forceinline__ void get(float* f) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <bool NT> __device__ __forceinline__ void put(float* p, const float* f) {
+  put16<NT>(p, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+  put16<NT>(p + 4, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
+}
+template <bool NT> __device__ __forceinline__ void put(uint16_t* p, const float* f) {
+  put16<NT>(p, make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])));
+}
+
+// One row per block of `waves` wavefronts; lane i of the block holds the chunks
+// i, i + 64 waves, ... (VPL of them).
+template <typename T, typename TW, int VPL, bool NT>
+__global__ __launch_bounds__(kMaxWaves * 64) void add_rms_norm_kernel(const T* x, const T* residual,
+                                                                     const TW* __restrict__ weight, float eps, int H,
+                                                                     T* h_out, T* y, uint8_t* __restrict__ y8,
+                                                                     float* __restrict__ scales) {
+  __shared__ float2 red[kMaxWaves];
   const int64_t base = static_cast<int64_t>(blockIdx.x) * H;
+  const int threads = blockDim.x;
+  Chunk<T> cx[VPL], cr[VPL];
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    const int c = (v * threads + threadIdx.x) * 8;
+    if (c < H) {
+      cx[v].template load<NT>(x + base + c);
+      if (residual) cr[v].template load<NT>(residual + base + c);
+    }
+  }
   float h[VPL][8];
   float ss = 0.f;
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
-    const int c = (v * WAVES * 64 + threadIdx.x) * 8;
+    const int c = (v * threads + threadIdx.x) * 8;
     if (c < H) {
-      load8(x + base + c, h[v]);
+      cx[v].get(h[v]);
       if (residual) {
         float r[8];
-        load8(residual + base + c, r);
+        cr[v].get(r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[v][i] = as_stored<T>(h[v][i] + r[i]);
+        if (h_out) put<NT>(h_out + base + c, h[v]);
+      } else if (h_out) {
+        put<NT>(h_out + base + c, h[v]);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(h[v][i], h[v][i], ss);
     }
   }
-  const float r = 1.0f / sqrtf(block_sum<WAVES>(ss, red) / static_cast<float>(H) + eps);
+  if (!y && !y8) return;
+  const float r = 1.0f / sqrtf(block_sum(ss, 0.f, threads >> 6, red).x / static_cast<float>(H) + eps);
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
-    const int c = (v * WAVES * 64 + threadIdx.x) * 8;
+    const int c = (v * threads + threadIdx.x) * 8;
     if (c < H) {
-      if (h_out) store8(h_out + base + c, h[v]);
       float w[8];
       load8(weight + c, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[v][i] = h[v][i] * r * w[i];
-      if (y) store8(y + base + c, h[v]);
+      if (y) put<NT>(y + base + c, h[v]);
       if (y8) {
         float amax = 0.f;
 #pragma unroll
@@ -86,79 +149,123 @@ __global__ __launch_bounds__(WAVES * 64) void add_rms_norm_kernel(const T* x, co
 
 // Rows of the backward that one block walks: block b takes rows b, b + G, ...
 // and keeps its share of d_w in registers, written once as row b of the
-// workspace [G, H].
-constexpr int kBwBlocks = 512;
-inline int bw_blocks(int T) { return T < kBwBlocks ? T : kBwBlocks; }
+// workspace [G, H].  The next row's loads are issued before this row's sums.
+// 16384 x 4096 bf16 in us, 512 / 1024 blocks: 95 / 91 with the reduction's 5;
+// 1001 x 1408 fp32, 512 / 768 / 1024: 10 / 11 / 12.
+inline int bw_blocks(int T) {
+  const int most = T >= 8192 ? 1024 : 512;
+  return T < most ? T : most;
+}
 
-template <typename T, typename TW, int WAVES, int VPL>
-__global__ __launch_bounds__(WAVES * 64) void add_rms_norm_bw_kernel(const T* dy, const T* h, const T* dh,
-                                                                    const TW* __restrict__ weight, float eps,
-                                                                    int rows, int H, T* dx,
-                                                                    float* __restrict__ part) {
-  __shared__ float red[2][WAVES];
+template <typename T, typename TW, int VPL, bool NT>
+__global__ __launch_bounds__(kMaxWaves * 64) void add_rms_norm_bw_kernel(const T* dy, const T* h, const T* dh,
+                                                                        const TW* __restrict__ weight, float eps,
+                                                                        int rows, int H, T* dx,
+                                                                        float* __restrict__ part) {
+  // (fp32 rows of two chunks a lane leave no registers for it)
+  constexpr bool kAhead = !(sizeof(T) == 4 && VPL > 1);
+  __shared__ float2 red[2][kMaxWaves];
+  const int threads = blockDim.x;
   float dw[VPL][8] = {};
-  for (int t = blockIdx.x; t < rows; t += gridDim.x) {
+  Chunk<TW> w[VPL];
+  struct Row {
+    Chunk<T> h, dy, dh;
+  } cur[VPL], next[VPL];
+  auto fetch = [&](Row (&to)[VPL], int t) {
     const int64_t base = static_cast<int64_t>(t) * H;
-    float hv[VPL][8], g[VPL][8];
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      const int c = (v * threads + threadIdx.x) * 8;
+      if (c < H) {
+        to[v].h.template load<NT>(h + base + c);
+        to[v].dy.template load<NT>(dy + base + c);
+        if (dh) to[v].dh.template load<NT>(dh + base + c);
+      }
+    }
+  };
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    const int c = (v * threads + threadIdx.x) * 8;
+    if (c < H) w[v].template load<false>(weight + c);
+  }
+  fetch(cur, blockIdx.x);
+  int parity = 0;
+  for (int t = blockIdx.x; t < rows; t += gridDim.x) {
+    if (kAhead && t + static_cast<int>(gridDim.x) < rows) fetch(next, t + gridDim.x);
+    if (!kAhead && t != static_cast<int>(blockIdx.x)) fetch(cur, t);
+    const int64_t base = static_cast<int64_t>(t) * H;
     float ss = 0.f, dot = 0.f;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-      const int c = (v * WAVES * 64 + threadIdx.x) * 8;
+      const int c = (v * threads + threadIdx.x) * 8;
       if (c < H) {
-        float w[8];
-        load8(h + base + c, hv[v]);
-        load8(dy + base + c, g[v]);
-        load8(weight + c, w);
+        float hv[8], g[8], wv[8];
+        cur[v].h.get(hv);
+        cur[v].dy.get(g);
+        w[v].get(wv);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          ss = fmaf(hv[v][i], hv[v][i], ss);
-          dot = fmaf(hv[v][i], g[v][i] * w[i], dot);
+          ss = fmaf(hv[i], hv[i], ss);
+          dot = fmaf(hv[i], g[i] * wv[i], dot);
         }
       }
     }
-    const float r = 1.0f / sqrtf(block_sum<WAVES>(ss, red[0]) / static_cast<float>(H) + eps);
-    const float k = block_sum<WAVES>(dot, red[1]) * r / static_cast<float>(H);   // mean(w dy n)
+    const float2 s = block_sum(ss, dot, threads >> 6, red[parity]);
+    parity ^= 1;
+    const float r = 1.0f / sqrtf(s.x / static_cast<float>(H) + eps);
+    const float k = s.y * r / static_cast<float>(H);   // mean(w dy n)
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-      const int c = (v * WAVES * 64 + threadIdx.x) * 8;
+      const int c = (v * threads + threadIdx.x) * 8;
       if (c < H) {
-        float w[8], o[8];
-        load8(weight + c, w);
-        if (dh) load8(dh + base + c, o);
+        float hv[8], g[8], wv[8], o[8];
+        cur[v].h.get(hv);
+        cur[v].dy.get(g);
+        w[v].get(wv);
+        if (dh) cur[v].dh.get(o);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float n = hv[v][i] * r;
-          dw[v][i] = fmaf(g[v][i], n, dw[v][i]);
-          const float d = r * (g[v][i] * w[i] - n * k);
+          const float n = hv[i] * r;
+          dw[v][i] = fmaf(g[i], n, dw[v][i]);
+          const float d = r * (g[i] * wv[i] - n * k);
           o[i] = dh ? o[i] + d : d;
         }
-        store8(dx + base + c, o);
+        put<NT>(dx + base + c, o);
       }
+      if constexpr (kAhead) cur[v] = next[v];
     }
   }
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
-    const int c = (v * WAVES * 64 + threadIdx.x) * 8;
+    const int c = (v * threads + threadIdx.x) * 8;
     if (c < H) store8(part + static_cast<int64_t>(blockIdx.x) * H + c, dw[v]);
   }
 }
 
-// d_w[c] = sum_b part[b, c]: a block takes 64 columns, its 16 waves every 16th
-// row; the waves' sums meet in LDS and are added in wave order.
-constexpr int kRedWaves = 16;
-__global__ __launch_bounds__(kRedWaves * 64) void reduce_dw_kernel(const float* __restrict__ part, int nblk, int H,
-                                                                  float* __restrict__ dw) {
-  __shared__ float red[kRedWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
-  float s = 0.f;
+// d_w[c] = sum_b part[b, c]: a block takes 32 columns; 8 lanes of four columns
+// side by side, 32 of those take every 32nd row, and their sums are added in
+// order from LDS.
+constexpr int kRedCols = 32, kRedRows = 32;
+__global__ __launch_bounds__(256) void reduce_dw_kernel(const float* __restrict__ part, int nblk, int H,
+                                                        float* __restrict__ dw) {
+  __shared__ float4 red[kRedRows][kRedCols / 4];
+  const int q = threadIdx.x % (kRedCols / 4), r = threadIdx.x / (kRedCols / 4);
+  const int c = blockIdx.x * kRedCols + q * 4;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (c < H)
-    for (int b = wave; b < nblk; b += kRedWaves) s += part[static_cast<int64_t>(b) * H + c];
-  red[wave][lane] = s;
+#pragma unroll 8
+    for (int b = r; b < nblk; b += kRedRows) {
+      const float4 v = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(b) * H + c);
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+  red[r][q] = s;
   __syncthreads();
-  if (wave == 0 && c < H) {
-    for (int i = 1; i < kRedWaves; ++i) s += red[i][lane];
-    dw[c] = s;
+  if (threadIdx.x < kRedCols && blockIdx.x * kRedCols + static_cast<int>(threadIdx.x) < H) {
+    const float* col = reinterpret_cast<const float*>(red) + threadIdx.x;
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRedRows; ++i) t += col[i * kRedCols];
+    dw[blockIdx.x * kRedCols + threadIdx.x] = t;
   }
 }
 
@@ -172,21 +279,33 @@ struct FwArgs {
   hipStream_t stream;
 };
 
-template <typename T, typename TW, int WAVES, int VPL> void fw_launch(const FwArgs& a) {
-  add_rms_norm_kernel<T, TW, WAVES, VPL><<<a.T, WAVES * 64, 0, a.stream>>>(
+// Rows of this many bytes in all go past the caches.
+constexpr int64_t kStreamBytes = 32ll << 20;
+
+template <typename T, typename TW, int VPL, bool NT> void fw_launch(const FwArgs& a) {
+  const int waves = (a.H / 8 + 64 * VPL - 1) / (64 * VPL);
+  add_rms_norm_kernel<T, TW, VPL, NT><<<a.T, waves * 64, 0, a.stream>>>(
       static_cast<const T*>(a.x), static_cast<const T*>(a.residual), static_cast<const TW*>(a.weight), a.eps, a.H,
       static_cast<T*>(a.h_out), static_cast<T*>(a.y), a.y8, a.scales);
 }
 
-// WAVES so that a row is at most two chunks per lane.
 template <typename T, typename TW> void fw_pick(const FwArgs& a) {
+  const bool nt = static_cast<int64_t>(a.T) * a.H * static_cast<int64_t>(sizeof(T)) >= kStreamBytes;
+  // Few rows: a row on as many waves as it has chunks for.  Many: up to four
+  // chunks a lane, so that a compute unit holds more rows at once (8192 x 7168
+  // bf16 with residual to h and FP8, us: one chunk a lane 87, two 73.6, three
+  // 73.3, four 71.1 = 5.8 TB/s, seven 75; two with plain loads and stores 79,
+  // non-temporal loads only 79, stores only 76; codes stored past the
+  // caches too 73.0).
   const int chunks = a.H / 8;
-  if (chunks <= 64) fw_launch<T, TW, 1, 1>(a);
-  else if (chunks <= 128) fw_launch<T, TW, 2, 1>(a);
-  else if (chunks <= 256) fw_launch<T, TW, 4, 1>(a);
-  else if (chunks <= 512) fw_launch<T, TW, 4, 2>(a);
-  else if (chunks <= 1024) fw_launch<T, TW, 8, 2>(a);
-  else fw_launch<T, TW, 16, 2>(a);
+  if (!nt) {
+    if (chunks <= 64 * kMaxWaves) fw_launch<T, TW, 1, false>(a);
+    else fw_launch<T, TW, 2, false>(a);
+  } else {
+    if (chunks <= 256) fw_launch<T, TW, 1, true>(a);
+    else if (chunks <= 512) fw_launch<T, TW, 2, true>(a);
+    else fw_launch<T, TW, 4, true>(a);
+  }
 }
 
 struct BwArgs {
@@ -199,20 +318,17 @@ struct BwArgs {
   hipStream_t stream;
 };
 
-template <typename T, typename TW, int WAVES, int VPL> void bw_launch(const BwArgs& a) {
-  add_rms_norm_bw_kernel<T, TW, WAVES, VPL><<<a.nblk, WAVES * 64, 0, a.stream>>>(
+template <typename T, typename TW, int VPL, bool NT> void bw_launch(const BwArgs& a) {
+  const int waves = (a.H / 8 + 64 * VPL - 1) / (64 * VPL);
+  add_rms_norm_bw_kernel<T, TW, VPL, NT><<<a.nblk, waves * 64, 0, a.stream>>>(
       static_cast<const T*>(a.dy), static_cast<const T*>(a.h), static_cast<const T*>(a.dh),
       static_cast<const TW*>(a.weight), a.eps, a.T, a.H, static_cast<T*>(a.dx), a.part);
 }
 
 template <typename T, typename TW> void bw_pick(const BwArgs& a) {
-  const int chunks = a.H / 8;
-  if (chunks <= 64) bw_launch<T, TW, 1, 1>(a);
-  else if (chunks <= 128) bw_launch<T, TW, 2, 1>(a);
-  else if (chunks <= 256) bw_launch<T, TW, 4, 1>(a);
-  else if (chunks <= 512) bw_launch<T, TW, 4, 2>(a);
-  else if (chunks <= 1024) bw_launch<T, TW, 8, 2>(a);
-  else bw_launch<T, TW, 16, 2>(a);
+  const bool nt = static_cast<int64_t>(a.T) * a.H * static_cast<int64_t>(sizeof(T)) >= kStreamBytes;
+  if (a.H <= 64 * 8 * (sizeof(T) == 4 ? 16 : 8)) nt ? bw_launch<T, TW, 1, true>(a) : bw_launch<T, TW, 1, false>(a);
+  else nt ? bw_launch<T, TW, 2, true>(a) : bw_launch<T, TW, 2, false>(a);
 }
 
 inline bool norm_sizes(int T, int H) { return T >= 0 && H > 0; }
@@ -276,7 +392,7 @@ extern "C" moe_status moe_add_rms_norm_backward(const void* dy, const void* h, c
     }
     MOE_LAUNCH_CHECK();
   }
-  reduce_dw_kernel<<<(H + 63) / 64, kRedWaves * 64, 0, stream>>>(static_cast<const float*>(workspace),
+  reduce_dw_kernel<<<(H + kRedCols - 1) / kRedCols, 256, 0, stream>>>(static_cast<const float*>(workspace),
                                                                  T > 0 ? bw_blocks(T) : 0, H, d_weight);
   MOE_LAUNCH_CHECK();
   return MOE_OK;

@@ -1,4 +1,4 @@
-"""One GPU's MoE layer: device buffers plus the six entry points in order.
+"""One GPU's MoE layer: device buffers plus the entry points in order.
 
 torch provides device memory and the stream; every step of the layer runs
 in libmoe_ep.so:
@@ -7,6 +7,8 @@ in libmoe_ep.so:
       -> moe_grouped_gemm_w2 -> moe_combine
 
 or, unfused, moe_grouped_gemm_w13 (G) -> moe_silu_mul -> moe_grouped_gemm_w2.
+With 4-bit weights both products are moe_grouped_gemv_w4 (for decode steps);
+token rows that are in block FP8 already go through moe_permute_fp8.
 Buffers are sized from capacity bounds once, so a step never allocates and
 its launch shapes never depend on the routing.
 """
@@ -21,9 +23,11 @@ from . import (MOE_EPI_SILU_MUL, MOE_EPI_STORE_G, moe_combine, moe_dispatch_layo
                moe_grouped_gemm_workspace_bytes, moe_pack_w13, MOE_W_PACKED, MOE_W_ROW_MAJOR,
                moe_combine_backward, moe_silu_mul_backward, moe_permute_backward,
                moe_transpose_weights, moe_grouped_gemm_wgrad, moe_grouped_gemm_w13_silu_backward,
-               moe_permute, moe_silu_mul)
+               moe_permute, moe_silu_mul, MOE_W4_E2M1, MOE_W4_INT4, moe_grouped_gemv_w4, moe_pack_w4,
+               moe_permute_fp8)
 
 _TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.uint8}
+_W4 = {"int4": MOE_W4_INT4, "fp4": MOE_W4_E2M1}
 
 
 @dataclass(frozen=True)
@@ -37,8 +41,15 @@ class LayerShape:
     I: int
     R: int              # capacity per local expert, 0 = exact-fit
     act: str            # token activations: "f32" | "bf16"
-    wdt: str            # expert weights: "f32" | "bf16" | "fp8"
+    wdt: str            # expert weights: "f32" | "bf16" | "fp8" | "int4" | "fp4" (e2m1)
     BM: int = 128
+    x_fp8: bool = False  # token rows arrive in block FP8 (forward takes x_scales)
+
+    def __post_init__(self):
+        if self.x_fp8 and self.wdt in ("f32", "bf16"):
+            raise ValueError("FP8 token rows need FP8 or 4-bit weights")
+        if self.wdt in _W4 and self.act == "f32" and not self.x_fp8:
+            raise ValueError("4-bit weights take bf16 or FP8 rows")
 
     @property
     def rows_cap(self) -> int:
@@ -46,7 +57,7 @@ class LayerShape:
 
     @property
     def buf_dt(self) -> str:
-        return "fp8" if self.wdt == "fp8" else self.act
+        return "fp8" if self.wdt == "fp8" or self.x_fp8 else self.act
 
     @property
     def z_dt(self) -> str:
@@ -73,9 +84,10 @@ class MoELayer:
         ws = moe_dispatch_layout_workspace_bytes(s.T, s.K, s.L)
         self.workspace = torch.zeros(max(ws, 4), dtype=torch.uint8, device=dev)
         # K-split partial sums of the GEMMs' last round (both GEMMs run on one
-        # stream, one after the other, so they share it)
-        self.gemm_workspace = torch.empty(moe_grouped_gemm_workspace_bytes(), dtype=torch.uint8,
-                                          device=dev)
+        # stream, one after the other, so they share it; the 4-bit products
+        # have none)
+        self.gemm_workspace = torch.empty(0 if s.wdt in _W4 else moe_grouped_gemm_workspace_bytes(),
+                                          dtype=torch.uint8, device=dev)
         self.buf = torch.empty(rc, s.H, dtype=_TORCH[s.buf_dt], device=dev)
         self.buf_scales = (torch.empty(rc, s.H // 128, dtype=torch.float32, device=dev)
                            if s.buf_dt == "fp8" else None)
@@ -86,6 +98,7 @@ class MoELayer:
         self.out = torch.empty(rc, s.H, dtype=_TORCH[s.out_dt], device=dev)
         self.y = torch.empty(s.T, s.H, dtype=_TORCH[s.out_dt], device=dev)
         self.w13 = self.w13_scales = self.w2 = self.w2_scales = self.w13_packed = None
+        self.w4 = None                                       # packed 4-bit weights: (codes, scales) of W13 and W2
 
     def set_fused(self, fused: bool):
         """Switch the gate/up GEMM between the fused SiLU*up epilogue (the
@@ -103,7 +116,18 @@ class MoELayer:
     def set_weights(self, w13, w2, w13_scales=None, w2_scales=None, pack_w13=True):
         """Device weights in the pages' layouts.  With pack_w13 (the default)
         the gate/up weights are also packed once into the GEMM's staging
-        order (moe_pack_w13), which the gate/up GEMM then reads."""
+        order (moe_pack_w13), which the gate/up GEMM then reads.
+
+        4-bit layers: w13 [L,2I,H/2] and w2 [L,H,I/2] are codes (uint8, two a
+        byte), the scales [L,2I,H/group] and [L,H,I/group] (fp32 or bf16);
+        both are packed (moe_pack_w4), and only the packed copies are kept."""
+        if self.shape.wdt in _W4:
+            self.w4 = []
+            for codes, scales in ((w13, w13_scales), (w2, w2_scales)):
+                packed = torch.empty_like(codes), torch.empty_like(scales)
+                moe_pack_w4(codes, scales, _W4[self.shape.wdt], *packed)
+                self.w4.append(packed)
+            return
         self.w13, self.w2, self.w13_scales, self.w2_scales = w13, w2, w13_scales, w2_scales
         self.w13_packed = None
         if pack_w13:
@@ -117,28 +141,36 @@ class MoELayer:
                             self.offsets, self.slot_of, self.row_src, self.tile_offsets,
                             self.dev_status, self.workspace)
 
-    def permute(self, x):
-        moe_permute(x, self.slot_of, self.buf, self.buf_scales)
+    def permute(self, x, x_scales=None, bind=False):
+        if self.shape.x_fp8:
+            if x_scales is None:
+                raise ValueError("x_scales is required for FP8 token rows")
+            return moe_permute_fp8(x, x_scales, self.slot_of, self.buf, self.buf_scales, bind=bind)
+        if x_scales is not None:
+            raise ValueError("x_scales goes with FP8 token rows (LayerShape.x_fp8)")
+        return moe_permute(x, self.slot_of, self.buf, self.buf_scales, bind=bind)
 
-    def gemm_w13(self):
+    def gemm_w13(self, bind=False):
+        epi, out, scales = ((MOE_EPI_SILU_MUL, self.z, self.z_scales) if self.fused
+                            else (MOE_EPI_STORE_G, self.g, None))
+        if self.w4 is not None:
+            return moe_grouped_gemv_w4(self.buf, self.buf_scales, *self.w4[0], _W4[self.shape.wdt], self.counts,
+                                       self.offsets, epi, out, bind=bind)
         w, lay = ((self.w13_packed, MOE_W_PACKED) if self.w13_packed is not None
                   else (self.w13, MOE_W_ROW_MAJOR))
-        if self.fused:
-            moe_grouped_gemm_w13(self.buf, self.buf_scales, w, self.w13_scales, self.counts,
-                                 self.offsets, MOE_EPI_SILU_MUL, self.z, self.z_scales,
-                                 workspace=self.gemm_workspace, w13_layout=lay)
-        else:
-            moe_grouped_gemm_w13(self.buf, self.buf_scales, w, self.w13_scales, self.counts,
-                                 self.offsets, MOE_EPI_STORE_G, self.g,
-                                 workspace=self.gemm_workspace, w13_layout=lay)
+        return moe_grouped_gemm_w13(self.buf, self.buf_scales, w, self.w13_scales, self.counts, self.offsets, epi,
+                                    out, scales, workspace=self.gemm_workspace, w13_layout=lay, bind=bind)
 
     def silu_mul(self):
         if not self.fused:
             moe_silu_mul(self.g, self.counts, self.offsets, self.z, self.z_scales)
 
-    def gemm_w2(self):
-        moe_grouped_gemm_w2(self.z, self.z_scales, self.w2, self.w2_scales, self.counts,
-                            self.offsets, self.out, workspace=self.gemm_workspace)
+    def gemm_w2(self, bind=False):
+        if self.w4 is not None:
+            return moe_grouped_gemv_w4(self.z, self.z_scales, *self.w4[1], _W4[self.shape.wdt], self.counts,
+                                       self.offsets, MOE_EPI_STORE_G, self.out, bind=bind)
+        return moe_grouped_gemm_w2(self.z, self.z_scales, self.w2, self.w2_scales, self.counts,
+                                   self.offsets, self.out, workspace=self.gemm_workspace, bind=bind)
 
     def combine(self, topk_weights):
         moe_combine(self.out, self.slot_of, topk_weights, self.y)
@@ -149,7 +181,7 @@ class MoELayer:
         transposed again when set_weights installs new tensors; in-place
         updates need refresh_transposed_weights)."""
         s = self.shape
-        if s.wdt == "fp8":
+        if s.wdt not in ("f32", "bf16"):
             raise ValueError("the backward covers bf16 and fp32 layers")
         dev = self.buf.device
         gdt = self.out.dtype                       # gradients stored like the expert output
@@ -237,44 +269,34 @@ class MoELayer:
             f()
         return self.dx, self.d_w
 
-    def bind_forward(self, x, topk_ids, topk_weights):
+    def bind_forward(self, x, topk_ids, topk_weights, x_scales=None):
         """The forward's launches as (name, callable) pairs, each marshalled
         once (shapes checked, pointers and the current stream looked up), so
         calling them runs the path with a few microseconds of host time per
         launch.  The tensors must stay alive and unchanged in shape."""
         s = self.shape
-        w, lay = ((self.w13_packed, MOE_W_PACKED) if self.w13_packed is not None
-                  else (self.w13, MOE_W_ROW_MAJOR))
         st = [
             ("layout", moe_dispatch_layout(topk_ids, s.E, s.expert_begin, s.L, s.R, s.BM, self.counts,
                                            self.offsets, self.slot_of, self.row_src, self.tile_offsets,
                                            self.dev_status, self.workspace, bind=True)),
-            ("permute", moe_permute(x, self.slot_of, self.buf, self.buf_scales, bind=True)),
+            ("permute", self.permute(x, x_scales, bind=True)),
+            ("gemm_w13", self.gemm_w13(bind=True)),
         ]
-        if self.fused:
-            st.append(("gemm_w13", moe_grouped_gemm_w13(self.buf, self.buf_scales, w, self.w13_scales,
-                                                         self.counts, self.offsets, MOE_EPI_SILU_MUL, self.z,
-                                                         self.z_scales, workspace=self.gemm_workspace,
-                                                         w13_layout=lay, bind=True)))
-        else:
-            st.append(("gemm_w13", moe_grouped_gemm_w13(self.buf, self.buf_scales, w, self.w13_scales,
-                                                         self.counts, self.offsets, MOE_EPI_STORE_G, self.g,
-                                                         workspace=self.gemm_workspace, w13_layout=lay,
-                                                         bind=True)))
+        if not self.fused:
             st.append(("silu_mul", moe_silu_mul(self.g, self.counts, self.offsets, self.z, self.z_scales,
                                                 bind=True)))
         st += [
-            ("gemm_w2", moe_grouped_gemm_w2(self.z, self.z_scales, self.w2, self.w2_scales, self.counts,
-                                            self.offsets, self.out, workspace=self.gemm_workspace,
-                                            bind=True)),
+            ("gemm_w2", self.gemm_w2(bind=True)),
             ("combine", moe_combine(self.out, self.slot_of, topk_weights, self.y, bind=True)),
         ]
         return st
 
-    def forward(self, x, topk_ids, topk_weights):
-        """The whole path on the current stream; returns y [T,H] (no sync)."""
+    def forward(self, x, topk_ids, topk_weights, x_scales=None):
+        """The whole path on the current stream; returns y [T,H] (no sync).
+        x: [T,H] activations, or with LayerShape.x_fp8 e4m3fn codes with
+        x_scales [T,H/128] (as moe_add_rms_norm writes them)."""
         self.layout(topk_ids)
-        self.permute(x)
+        self.permute(x, x_scales)
         self.gemm_w13()
         self.silu_mul()
         self.gemm_w2()
