@@ -635,67 +635,99 @@ __global__ __launch_bounds__(kThreads) void group_topk_seg_kernel(RouteArgs a) {
   }
 }
 
-// Backward: one wavefront per token.  Lane k holds route k's id, score and
-// ds; the row's other elements are 0 (sigmoid) or the softmax's -s_e dot.
-template <int NPL, bool SIG>
+// The sum over this lane's run of SEG (16 or 32) lanes, in every lane of it.
+template <int CTRL> __device__ __forceinline__ double dpp_f64(double v) {
+  const int64_t u = __double_as_longlong(v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, 0xF, 0xF, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, 0xF, 0xF, true);
+  return __longlong_as_double(static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo));
+}
+template <int SEG> __device__ __forceinline__ double seg_sum_f64(double v) {
+  v += dpp_f64<moe_router::kDppXor1>(v);
+  v += dpp_f64<moe_router::kDppXor2>(v);
+  v += dpp_f64<moe_router::kDppHalfMirror>(v);
+  v += dpp_f64<moe_router::kDppMirror>(v);
+  if constexpr (SEG == 32) v += __shfl_xor(v, 16);
+  return v;
+}
+
+// Backward: a wave takes 64 / SEG tokens.  The routes' part is computed for all
+// of them at once, route k of token i in lane i SEG + k; then the wave writes
+// the rows one after the other: 0 (sigmoid) or the softmax's -s_e dot, plus what
+// the routes add.  The routes' part is in fp64: with renormalised weights the
+// terms of ds cancel (all of them for K = 1, and the softmax's sum_k ds_k w_k
+// vanishes).  With one token a wave that part, in which 6 or 8 of 64 lanes
+// work, bound the kernel (8192 x 256, K = 8: 6.9 us).
+template <int NPL, bool SIG, int SEG>
 __global__ __launch_bounds__(kThreads) void group_topk_bw_kernel(RouteArgs a, const float* __restrict__ d_weights,
                                                                  float* __restrict__ d_logits) {
+  constexpr int kTok = MOE_WAVE / SEG;
   const int lane = moe::lane_id();
-  const int t = blockIdx.x * kWaves + (threadIdx.x >> 6);
-  if (t >= a.T) return;
-  const float* row = a.logits + static_cast<int64_t>(t) * a.E;
-  float l[NPL];
-  float m = 0.f, sum = 1.f;
-  if (!SIG) {
-    m = -INFINITY;
-    each<NPL>([&](auto j) {
-      const int e = lane + MOE_WAVE * j;
-      l[j] = e < a.E ? row[e] : -INFINITY;
-      if (!(l[j] <= kMask)) m = fmaxf(m, l[j]);
+  const int seg = lane / SEG, sl = lane % SEG;
+  const int t0 = (blockIdx.x * kWaves + (threadIdx.x >> 6)) * kTok;
+  if (t0 >= a.T) return;
+  const int e0 = lane * NPL;
+  float p[kTok][NPL];
+  float m = 0.f, sum = 1.f;                     // of this lane's own token
+  if constexpr (!SIG) {
+    each<kTok>([&](auto i) {
+      const float* row = a.logits + static_cast<int64_t>(min(t0 + i, a.T - 1)) * a.E;
+      each<NPL>([&](auto j) { p[i][j] = e0 + j < a.E ? row[e0 + j] : -INFINITY; });
     });
-    m = wave_max_f32(m);
-    sum = 0.f;
-    each<NPL>([&](auto j) {
-      l[j] = l[j] <= kMask ? 0.f : expf(l[j] - m);
-      sum += l[j];
+    each<kTok>([&](auto i) {
+      float mi = -INFINITY, si = 0.f;
+      each<NPL>([&](auto j) { mi = p[i][j] <= kMask ? mi : fmaxf(mi, p[i][j]); });
+      mi = wave_max_f32(mi);
+      each<NPL>([&](auto j) {
+        p[i][j] = p[i][j] <= kMask ? 0.f : expf(p[i][j] - mi);
+        si += p[i][j];
+      });
+      si = wave_sum_f32(si);
+      const float inv = si == 0.f ? 0.f : 1.0f / si;
+      each<NPL>([&](auto j) { p[i][j] *= inv; });
+      m = seg == i ? mi : m;
+      sum = seg == i ? si : sum;
     });
-    sum = wave_sum_f32(sum);
-    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-    each<NPL>([&](auto j) {
-      l[j] *= inv;
-    });      // s
   }
-  int id = lane < a.K ? a.ids[static_cast<int64_t>(t) * a.K + lane] : -1;
+  const int t = t0 + seg;
+  const bool on = t < a.T && sl < a.K;
+  int id = on ? a.ids[static_cast<int64_t>(t) * a.K + sl] : -1;
   if (id >= a.E) id = -1;
-  float s = 0.f, d = 0.f;
+  double s = 0.0, d = 0.0;
   if (id >= 0) {
-    const float x = row[id];
-    if (!(x <= kMask)) s = SIG ? sigmoid_f(x) : expf(x - m) / sum;
-    d = d_weights[static_cast<int64_t>(t) * a.K + lane] * a.scale;
+    const float x = a.logits[static_cast<int64_t>(t) * a.E + id];
+    if (!(x <= kMask)) s = SIG ? 1.0 / (1.0 + exp(-static_cast<double>(x))) : static_cast<double>(expf(x - m) / sum);
+    d = static_cast<double>(d_weights[static_cast<int64_t>(t) * a.K + sl]) * static_cast<double>(a.scale);
   }
   if (a.renorm) {
-    const float S = wave_sum_f32(s) + 1e-20f;
-    const float dot = wave_sum_f32(d * s) / S;
-    d = id >= 0 ? (d - dot) / S : 0.f;
+#pragma clang fp contract(off)
+    const double S = seg_sum_f64<SEG>(s) + 1e-20;
+    const double mean = seg_sum_f64<SEG>(d * s) / S;
+    d = id >= 0 ? (d - mean) / S : 0.0;
   }
   // g: what route k adds to its expert's element
-  const float dot = SIG ? 0.f : wave_sum_f32(d * s);
-  const float g = SIG ? d * s * (1.0f - s) : d * s;
-  float o[NPL];
-  each<NPL>([&](auto j) {
-    o[j] = SIG ? 0.f : -l[j] * dot;
-  });
-  for (int k = 0; k < a.K; ++k) {
-    const int e = __builtin_amdgcn_readlane(id, k);
-    if (e < 0) continue;
-    const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g), k));
-    each<NPL>([&](auto j) {
-      if (e == lane + MOE_WAVE * j) o[j] += v;
-    });
-  }
-  each<NPL>([&](auto j) {
-    const int e = lane + MOE_WAVE * j;
-    if (e < a.E) d_logits[static_cast<int64_t>(t) * a.E + e] = o[j];
+  const float dot = SIG ? 0.f : static_cast<float>(seg_sum_f64<SEG>(d * s));
+  const float g = static_cast<float>(SIG ? d * s * (1.0 - s) : d * s);
+  each<kTok>([&](auto i) {
+    if (t0 + i >= a.T) return;
+    float o[NPL];
+    const float di = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(dot), i * SEG));
+    each<NPL>([&](auto j) { o[j] = SIG ? 0.f : -p[i][j] * di; });
+    for (int k = 0; k < a.K; ++k) {
+      const int e = __builtin_amdgcn_readlane(id, i * SEG + k);
+      const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g), i * SEG + k));
+      each<NPL>([&](auto j) { o[j] += e == e0 + j ? v : 0.f; });
+    }
+    float* out = d_logits + static_cast<int64_t>(t0 + i) * a.E;
+    if (NPL % 4 == 0 && a.vec) {
+      if (e0 < a.E)
+        for (int j = 0; j < NPL; j += 4)
+          *reinterpret_cast<float4*>(out + e0 + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+    } else {
+      each<NPL>([&](auto j) {
+        if (e0 + j < a.E) out[e0 + j] = o[j];
+      });
+    }
   });
 }
 
@@ -726,10 +758,17 @@ template <int NPL> void launch_fw(RouteArgs a, hipStream_t stream) {
     else group_topk_kernel<NPL, false, false><<<grid, kThreads, shared, stream>>>(a);
   }
 }
-template <int NPL> void launch_bw(const RouteArgs& a, const float* dw, float* dl, hipStream_t stream) {
-  const int grid = (a.T + kWaves - 1) / kWaves;
-  if (a.sigmoid) group_topk_bw_kernel<NPL, true><<<grid, kThreads, 0, stream>>>(a, dw, dl);
-  else group_topk_bw_kernel<NPL, false><<<grid, kThreads, 0, stream>>>(a, dw, dl);
+template <int NPL> void launch_bw(RouteArgs a, const float* dw, float* dl, hipStream_t stream) {
+  a.vec = a.E % NPL == 0 && aligned16(dl);
+  const bool wide = a.K > 16;
+  const int tok = kWaves * (wide ? 2 : 4), grid = (a.T + tok - 1) / tok;
+  if (a.sigmoid) {
+    if (wide) group_topk_bw_kernel<NPL, true, 32><<<grid, kThreads, 0, stream>>>(a, dw, dl);
+    else group_topk_bw_kernel<NPL, true, 16><<<grid, kThreads, 0, stream>>>(a, dw, dl);
+  } else {
+    if (wide) group_topk_bw_kernel<NPL, false, 32><<<grid, kThreads, 0, stream>>>(a, dw, dl);
+    else group_topk_bw_kernel<NPL, false, 16><<<grid, kThreads, 0, stream>>>(a, dw, dl);
+  }
 }
 
 }  // namespace
