@@ -111,22 +111,20 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: _stream(torch.empty(0, device=torch.device("cuda", dev))))
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_CALL = {name: getattr(block_lib, name) for name in _SIG}
+
+
 def _run(fn: str, bind: bool, dev: int, args: tuple):
     """Call C entry point ``fn`` with device ``dev`` current (launches go to the
     current device), or return that call as a zero-argument callable."""
-    f = getattr(block_lib, fn)
-
     if bind:
-        return lambda: _run_now(fn, f, dev, args)
-    return _run_now(fn, f, dev, args)
-
-
-def _run_now(fn, f, dev, args):
-    if torch.cuda.current_device() == dev:
-        st = f(*args)
+        return lambda: _run(fn, False, dev, args)
+    if _current_device() == dev:
+        st = _CALL[fn](*args)
     else:
         with torch.cuda.device(dev):
-            st = f(*args)
+            st = _CALL[fn](*args)
     if st != 0:
         raise MoEError(fn, st)
 

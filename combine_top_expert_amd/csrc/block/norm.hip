@@ -151,9 +151,14 @@ __global__ __launch_bounds__(kMaxWaves * 64) void add_rms_norm_kernel(const T* x
 // and keeps its share of d_w in registers, written once as row b of the
 // workspace [G, H].  The next row's loads are issued before this row's sums.
 // 16384 x 4096 bf16 in us, 512 / 1024 blocks: 95 / 91 with the reduction's 5;
-// 1001 x 1408 fp32, 512 / 768 / 1024: 10 / 11 / 12.
-inline int bw_blocks(int T) {
-  const int most = T >= 8192 ? 1024 : 512;
+// 1001 x 1408 fp32, 512 / 768 / 1024: 10 / 11 / 12.  Narrow rows have few waves
+// a block and get more blocks, with 32 rows each at least (65536 x 512 bf16,
+// 1024 / 2048 / 4096 blocks: 66 / 57 / 59; 32768 x 1408, 1024 / 2048: 68 / 82).
+inline int bw_blocks(int T, int H) {
+  const int waves = (H / 8 + 63) / 64;
+  const int base = T >= 8192 ? 1024 : 512;
+  const int narrow = 4096 / waves < T / 32 ? 4096 / waves : T / 32;
+  const int most = base > narrow ? base : narrow;
   return T < most ? T : most;
 }
 
@@ -243,18 +248,19 @@ __global__ __launch_bounds__(kMaxWaves * 64) void add_rms_norm_bw_kernel(const T
 }
 
 // d_w[c] = sum_b part[b, c]: a block takes 32 columns; 8 lanes of four columns
-// side by side, 32 of those take every 32nd row, and their sums are added in
-// order from LDS.
-constexpr int kRedCols = 32, kRedRows = 32;
-__global__ __launch_bounds__(256) void reduce_dw_kernel(const float* __restrict__ part, int nblk, int H,
-                                                        float* __restrict__ dw) {
-  __shared__ float4 red[kRedRows][kRedCols / 4];
+// side by side, ROWS of those take every ROWS-th row, and their sums are added
+// in order from LDS.
+constexpr int kRedCols = 32;
+template <int ROWS>
+__global__ __launch_bounds__(ROWS * 8) void reduce_dw_kernel(const float* __restrict__ part, int nblk, int H,
+                                                             float* __restrict__ dw) {
+  __shared__ float4 red[ROWS][kRedCols / 4];
   const int q = threadIdx.x % (kRedCols / 4), r = threadIdx.x / (kRedCols / 4);
   const int c = blockIdx.x * kRedCols + q * 4;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (c < H)
 #pragma unroll 8
-    for (int b = r; b < nblk; b += kRedRows) {
+    for (int b = r; b < nblk; b += ROWS) {
       const float4 v = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(b) * H + c);
       s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
     }
@@ -263,8 +269,8 @@ __global__ __launch_bounds__(256) void reduce_dw_kernel(const float* __restrict_
   if (threadIdx.x < kRedCols && blockIdx.x * kRedCols + static_cast<int>(threadIdx.x) < H) {
     const float* col = reinterpret_cast<const float*>(red) + threadIdx.x;
     float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < kRedRows; ++i) t += col[i * kRedCols];
+#pragma unroll 16
+    for (int i = 0; i < ROWS; ++i) t += col[i * kRedCols];
     dw[blockIdx.x * kRedCols + threadIdx.x] = t;
   }
 }
@@ -364,7 +370,7 @@ extern "C" moe_status moe_add_rms_norm(const void* x, const void* residual, moe_
 
 extern "C" size_t moe_add_rms_norm_backward_workspace_bytes(int T, int H) {
   if (!norm_sizes(T, H) || H % 8 != 0 || H > kMaxH) return 0;
-  return static_cast<size_t>(bw_blocks(T)) * H * sizeof(float);
+  return static_cast<size_t>(bw_blocks(T, H)) * H * sizeof(float);
 }
 
 extern "C" moe_status moe_add_rms_norm_backward(const void* dy, const void* h, const void* dh, moe_dtype dt,
@@ -382,7 +388,7 @@ extern "C" moe_status moe_add_rms_norm_backward(const void* dy, const void* h, c
     MOE_CHECK(aligned16(dy) && aligned16(h) && aligned16(dh) && aligned16(weight) && aligned16(dx) && aligned16(workspace),
               MOE_ERR_INVALID_ARG);
     MOE_CHECK(workspace_bytes >= need, MOE_ERR_WORKSPACE);
-    const BwArgs a{dy, h, dh, weight, eps, T, H, dx, static_cast<float*>(workspace), bw_blocks(T), stream};
+    const BwArgs a{dy, h, dh, weight, eps, T, H, dx, static_cast<float*>(workspace), bw_blocks(T, H), stream};
     if (dt == MOE_BF16) {
       if (w_dt == MOE_BF16) bw_pick<uint16_t, uint16_t>(a);
       else bw_pick<uint16_t, float>(a);
@@ -392,8 +398,10 @@ extern "C" moe_status moe_add_rms_norm_backward(const void* dy, const void* h, c
     }
     MOE_LAUNCH_CHECK();
   }
-  reduce_dw_kernel<<<(H + kRedCols - 1) / kRedCols, 256, 0, stream>>>(static_cast<const float*>(workspace),
-                                                                 T > 0 ? bw_blocks(T) : 0, H, d_weight);
+  const int nblk = T > 0 ? bw_blocks(T, H) : 0, grid = (H + kRedCols - 1) / kRedCols;
+  const float* part = static_cast<const float*>(workspace);
+  if (nblk <= 1024) reduce_dw_kernel<32><<<grid, 256, 0, stream>>>(part, nblk, H, d_weight);
+  else reduce_dw_kernel<128><<<grid, 1024, 0, stream>>>(part, nblk, H, d_weight);
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }

@@ -154,8 +154,8 @@ moe_status moe_permute_fp8(const void* x8, const float* x8_scales, int T, int K,
  * The packed copies have the same sizes and may not overlap the sources:
  *   codes  [L][N/16][K/128][64][16 bytes]: 16 rows x 128 columns are 1 KB; piece
  *          l holds of row l & 15 the columns 32 s + 8 (l >> 4) + 0..7 as its
- *          dword s (INT4: column 2i in nibble i, 2i + 1 in nibble i + 4;
- *          E2M1: in column order)
+ *          dword s (INT4: column 2i in bits 4 i + 3 .. 4 i + 6, 2 i + 1 sixteen
+ *          bits above, bit 32 being bit 0; E2M1: in column order)
  *   scales [L][N/16][K/128][128/group][16 rows]
  * Limits: N % 128 == 0, K % 128 == 0, group in {32, 64, 128}; codes and
  * codes_packed 16-byte, scales_packed 16-byte aligned.
