@@ -152,8 +152,11 @@ template <int FMT, bool FP8, typename TS, int SG, int MT> struct Block {
   // ahead (weights three stages ahead at two waves per SIMD: the same time to
   // 1 % for one or four rows, 2 to 8 % more on the down shape); 32 rows leave
   // no registers for the activations (168 at three waves per SIMD), which are
-  // fetched when their stage begins.
+  // fetched when their stage begins, and so are the scales where one load
+  // covers four stages (two registers spilled there cost 6 us of 88 at L 32,
+  // 4096 x 7168, in the 16-row path that does not use them).
   static constexpr bool kAhead = MT == 1;
+  static constexpr bool kScalesAhead = kAhead || CH < 4;
   struct Rows {
     Act<FP8> act[MT][4];
     float as[MT];
@@ -162,29 +165,33 @@ template <int FMT, bool FP8, typename TS, int SG, int MT> struct Block {
     uint4 w[kTiles];
   };
 
-  const uint8_t* w[kTiles];                     // uniform
-  const uint8_t* ap[MT];
-  const float* asp[MT];
-  const TS* sp;
+  // Addresses are a base that is the same for the wave plus 32 bits per lane:
+  // one register a lane and no arithmetic per load.
+  const uint8_t* w[kTiles];
+  const uint8_t* a;
+  const float* as;
+  const TS* sc;
+  uint32_t aoff[MT], asoff[MT], scoff, lane16;
   int KS, usub, lane;
   f32x4 acc[kTiles][MT];
 
   __device__ __forceinline__ void load_rows(Rows& r, int ks) const {
+    const uint8_t* at = a + static_cast<int64_t>(ks) * (128 * ESZ);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        r.act[m][s] = *reinterpret_cast<const Act<FP8>*>(ap[m] + static_cast<int64_t>(ks) * (128 * ESZ) + s * 32 * ESZ);
-      if constexpr (FP8) r.as[m] = asp[m][ks];
+      for (int s = 0; s < 4; ++s) r.act[m][s] = *reinterpret_cast<const Act<FP8>*>(at + aoff[m] + s * 32 * ESZ);
+      if constexpr (FP8) r.as[m] = *reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(as + ks) + asoff[m]);
     }
   }
   __device__ __forceinline__ void load(Buf& b, int ks) const {
 #pragma unroll
-    for (int f = 0; f < kTiles; ++f) b.w[f] = moe::load_nt16(w[f] + static_cast<int64_t>(ks) * 1024 + lane * 16);
+    for (int f = 0; f < kTiles; ++f) b.w[f] = moe::load_nt16(w[f] + static_cast<int64_t>(ks) * 1024 + lane16);
   }
   __device__ __forceinline__ f32x4 scales(int ks) const {
-    const int k = min(ks + usub, KS - 1);
-    return load_scales(sp + static_cast<int64_t>(k) * (SG * 16));
+    const uint32_t k = min(ks + usub, KS - 1);
+    return load_scales(reinterpret_cast<const TS*>(reinterpret_cast<const uint8_t*>(sc) +
+                                                   (scoff + k * (SG * 16 * static_cast<uint32_t>(sizeof(TS))))));
   }
 
   template <int SUB, int G, int F> __device__ __forceinline__ void fold(const f32x4& sc, const Rows& r, int m, const f32x4& c) {
@@ -263,8 +270,12 @@ template <int FMT, bool FP8, typename TS, int SG, int MT> struct Block {
                                        Rows (&r)[2]) {
     if (i >= n) return;
     if constexpr (U % CH == 0) {
-      sc = sc_next;
-      if (i + CH < n) sc_next = scales(ks_of(i + CH));
+      if constexpr (kScalesAhead) {
+        sc = sc_next;
+        if (i + CH < n) sc_next = scales(ks_of(i + CH));
+      } else {
+        sc = scales(ks_of(i));
+      }
     }
     if constexpr (kAhead) {
       if (i + 1 < n) load_rows(r[(U + 1) & 1], ks_of(i + 1));
@@ -287,15 +298,19 @@ template <int FMT, bool FP8, typename TS, int SG, int MT> struct Block {
     };
 #pragma unroll
     for (int f = 0; f < kTiles; ++f) w[f] = p.codes + tile(f) * KS * 1024;
+    lane16 = lane * 16;
     const int u = n >> 2;
     usub = u / SG;
-    sp = static_cast<const TS*>(p.scales) + (tile(n & 3) * KS * SG + u % SG) * 16 + j * 4;
+    sc = static_cast<const TS*>(p.scales) + tile(0) * KS * SG * 16;
+    scoff = static_cast<uint32_t>(((tile(n & 3) - tile(0)) * KS * SG + u % SG) * 16 + j * 4) * sizeof(TS);
+    a = p.a + row0 * p.K * ESZ;
+    if constexpr (FP8) as = p.a_scales + row0 * KS;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       // lanes past the last row read row 0 again; what they compute is not stored
-      const int64_t r = row0 + (m * 16 + n < rows ? m * 16 + n : 0);
-      ap[m] = p.a + (r * p.K + j * 8) * ESZ;
-      if constexpr (FP8) asp[m] = p.a_scales + r * KS;
+      const uint32_t r = m * 16 + n < rows ? m * 16 + n : 0;
+      aoff[m] = (r * p.K + j * 8) * ESZ;
+      asoff[m] = r * KS * 4;
 #pragma unroll
       for (int f = 0; f < kTiles; ++f) acc[f][m] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
@@ -422,7 +437,8 @@ template <int FMT, bool FP8> void launch_scale(const GemvArgs& p, int L, bool s3
 
 inline bool w4_sizes(int L, int N, int K) { return L >= 1 && N >= 1 && K >= 1; }
 inline bool w4_limits(int L, int N, int K, int group) {
-  return N % 128 == 0 && K % 128 == 0 && L <= 1024 && (group == 32 || group == 64 || group == 128);
+  return N % 128 == 0 && K % 128 == 0 && L <= 1024 && (group == 32 || group == 64 || group == 128) &&
+         static_cast<int64_t>(N) * K <= (1ll << 31) && K <= (1 << 24);   // 32-bit offsets within an expert
 }
 
 }  // namespace

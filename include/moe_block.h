@@ -157,8 +157,8 @@ moe_status moe_permute_fp8(const void* x8, const float* x8_scales, int T, int K,
  *          dword s (INT4: column 2i in bits 4 i + 3 .. 4 i + 6, 2 i + 1 sixteen
  *          bits above, bit 32 being bit 0; E2M1: in column order)
  *   scales [L][N/16][K/128][128/group][16 rows]
- * Limits: N % 128 == 0, K % 128 == 0, group in {32, 64, 128}; codes and
- * codes_packed 16-byte, scales_packed 16-byte aligned.
+ * Limits: N % 128 == 0, K % 128 == 0, N K <= 2^31, K <= 2^24, L <= 1024, group in
+ * {32, 64, 128}; codes, codes_packed and scales_packed 16-byte aligned.
  */
 moe_status moe_pack_w4(const void* codes, const void* scales, moe_dtype s_dt, moe_w4_format fmt, int L,
                        int N, int K, int group, void* codes_packed, void* scales_packed,
@@ -179,11 +179,11 @@ moe_status moe_pack_w4(const void* codes, const void* scales, moe_dtype s_dt, mo
  *   epi MOE_EPI_STORE_G: out [rows_cap,N] = G (gate/up or down products);
  *   MOE_EPI_SILU_MUL: out [rows_cap,N/2] = SiLU(G[:, :N/2]) * G[:, N/2:]
  *   out_dt in {F32, BF16}
- * Every count is right; weights are read once per 64 rows of an expert, so this
+ * Every count is right; weights are read once per 32 rows of an expert, so this
  * is the form for few rows per expert (moe_grouped_gemm_w13 / _w2 for many).
  * An infinite or NaN activation makes its row NaN.
- * Limits: N % 128 == 0, K % 128 == 0, L <= 1024, group in {32, 64, 128}; a,
- * codes_packed, scales_packed and out 16-byte aligned.
+ * Limits: N % 128 == 0, K % 128 == 0, N K <= 2^31, K <= 2^24, L <= 1024, group in
+ * {32, 64, 128}; a, codes_packed, scales_packed and out 16-byte aligned.
  */
 moe_status moe_grouped_gemv_w4(const void* a, moe_dtype a_dt, const float* a_scales,
                                const void* codes_packed, const void* scales_packed, moe_dtype s_dt,

@@ -142,6 +142,7 @@ def test_w4_refusals(ep):
                                                 K, epi, P(out), odt, None)
     for f in (pack, gemv):
         assert f(N=64) == UNSUPPORTED and f(K=192) == UNSUPPORTED and f(L=1025) == UNSUPPORTED
+        assert f(N=1 << 16, K=(1 << 15) + 128) == UNSUPPORTED and f(N=128, K=(1 << 24) + 128) == UNSUPPORTED
         assert f(group=16) == UNSUPPORTED and f(group=256) == UNSUPPORTED and f(group=0) == UNSUPPORTED
         assert f(sdt=FP8) == UNSUPPORTED and f(sdt=7) == INVALID and f(fmt=2) == INVALID
         assert f(L=0) == INVALID and f(N=0) == INVALID and f(K=-128) == INVALID
