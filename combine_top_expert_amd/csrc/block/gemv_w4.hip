@@ -2,10 +2,8 @@
 // weights, for few rows per expert.
 //
 // G[q,n] = sum_g scale[n,g] sum_{k in g} A[q,k] value(code[n,k]).  The 4-bit
-// values are exact in bf16 and go to the bf16 matrix cores as the first
-// operand (16 weight rows x 32 columns), up to 16 activation rows as the
-// second; a lane's four results are then four neighbouring weight rows of one
-// activation row.  Each scale group starts from a fresh accumulator, whose
+// values are exact in bf16 and go to the bf16 matrix cores (16 weight rows x 32
+// columns), with up to 16 activation rows as the other operand.  Each scale group starts from a fresh accumulator, whose
 // result is folded into fp32 sums with its scales.
 //
 // INT4 codes become 16 + code by placing the nibble in the mantissa of 16.0
@@ -18,6 +16,8 @@
 // Bound by reading the weights.  A workgroup's four waves share 64 weight rows
 // (four 16-row tiles) and split the columns in stages of 128; each streams its
 // share of the packed weights with 1 KB loads, and their sums meet in LDS.
+
+#include <type_traits>
 
 #include "block_common.h"
 
@@ -67,10 +67,11 @@ __global__ __launch_bounds__(256) void pack_scales_kernel(const TS* __restrict__
                                                           TS* __restrict__ out) {
   const int G = K / group, per = 128 / group;
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < count; i += gridDim.x * 256ll) {
-    const int r = static_cast<int>(i & 15);
-    const int g = static_cast<int>((i >> 4) % G);  // stage * per + group of the stage
-    const int64_t nt = (i >> 4) / G;
-    out[i] = scales[(nt * 16 + r) * G + g];
+    const int g = static_cast<int>(i % per);
+    const int r = static_cast<int>(i / per & 15);
+    const int64_t blk = i / per >> 4;             // (expert, row tile, stage)
+    const int ks = static_cast<int>(blk % (K / 128));
+    out[i] = scales[(blk / (K / 128) * 16 + r) * G + ks * per + g];
   }
 }
 
@@ -93,24 +94,47 @@ template <int FMT> __device__ __forceinline__ bf16x8 unpack(uint32_t v) {
   }
 }
 
-// 8 activations of one row as loaded, and as the matrix cores take them (e4m3
-// codes convert exactly)
-template <bool FP8> struct Act { uint4 v; };
-template <> struct Act<true> { uint2 v; };
-__device__ __forceinline__ bf16x8 act_bf16(const Act<false>& a) { return __builtin_bit_cast(bf16x8, a.v); }
-__device__ __forceinline__ bf16x8 act_bf16(const Act<true>& a) {
-  return as_bf16x8(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a.v.x, 1.0f, false)),
-                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a.v.x, 1.0f, true)),
-                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a.v.y, 1.0f, false)),
-                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a.v.y, 1.0f, true)));
+// 8 activations of one row as the matrix cores take them; e4m3 codes convert
+// exactly
+__device__ __forceinline__ bf16x8 as_rows(const uint4& v) { return __builtin_bit_cast(bf16x8, v); }
+__device__ __forceinline__ bf16x8 as_rows(const uint2& v) {
+  return as_bf16x8(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v.x, 1.0f, false)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v.x, 1.0f, true)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v.y, 1.0f, false)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v.y, 1.0f, true)));
 }
 
-__device__ __forceinline__ f32x4 load_scales(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
-__device__ __forceinline__ f32x4 load_scales(const uint16_t* p) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  return f32x4{__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-               __uint_as_float(v.y & 0xffff0000u)};
+__device__ __forceinline__ uint32_t dword(const uint4& v, int d) {
+  return d == 0 ? v.x : d == 1 ? v.y : d == 2 ? v.z : v.w;
 }
+
+// SG neighbouring scales as loaded
+template <typename TS, int SG> struct Scales {
+  TS v[SG];
+  __device__ __forceinline__ float get(int g) const {
+    if constexpr (sizeof(TS) == 4) return v[g];
+    else return __uint_as_float(static_cast<uint32_t>(v[g]) << 16);
+  }
+};
+template <> struct Scales<uint16_t, 2> {
+  uint32_t v;
+  __device__ __forceinline__ float get(int g) const { return __uint_as_float(g ? v & 0xffff0000u : v << 16); }
+};
+template <> struct Scales<uint16_t, 4> {
+  uint2 v;
+  __device__ __forceinline__ float get(int g) const {
+    const uint32_t w = g < 2 ? v.x : v.y;
+    return __uint_as_float(g & 1 ? w & 0xffff0000u : w << 16);
+  }
+};
+template <> struct Scales<float, 2> {
+  float2 v;
+  __device__ __forceinline__ float get(int g) const { return g ? v.y : v.x; }
+};
+template <> struct Scales<float, 4> {
+  float4 v;
+  __device__ __forceinline__ float get(int g) const { return g == 0 ? v.x : g == 1 ? v.y : g == 2 ? v.z : v.w; }
+};
 
 // the value that lane LANE of this lane's 16-lane row holds
 template <int LANE> __device__ __forceinline__ float row_bcast(float v) {
@@ -135,15 +159,186 @@ struct GemvArgs {
 constexpr int kPad = 4;                         // LDS row padding, floats
 constexpr int kRedStride = kTiles * 16 + kPad;
 
-// One column block (four weight tiles) of one expert, for one wave.
+// One column block (four weight tiles) of one expert for one wave, bf16 rows.
+//
+// Activations are the products' first operand and weights the second: lane
+// 16 j + n then holds, of every 16 x 16 result, weight row n and activation rows
+// 4 j .. 4 j + 3, and needs one scale per tile and group for its four values.
+template <int FMT, typename TS, int SG, int MT> struct BlockBf16 {
+  static constexpr int SPG = 4 / SG;            // 32-column steps of a scale group
+
+  struct Rows {                                 // a stage's activations as loaded
+    uint4 act[MT][4];
+  };
+  struct Weights {                              // a stage's weights
+    uint4 w[kTiles];
+  };
+  struct Sc {                                   // and their scales
+    Scales<TS, SG> s[kTiles];
+  };
+  // Up to 16 rows, everything is fetched one stage ahead (weights three stages
+  // ahead at two waves per SIMD: the same time to 1 % for one or four rows, 2 to
+  // 8 % more on the down shape); 32 rows leave no registers for the activations
+  // and scales (168 at three waves per SIMD), which are fetched when their stage
+  // begins; so are more than 8 bytes of scales a tile (INT4, whose offset takes
+  // registers too: more than one scale).
+  static constexpr bool kAhead = MT == 1;
+  static constexpr bool kScalesAhead = kAhead && (FMT == MOE_W4_INT4 ? SG == 1 : sizeof(Scales<TS, SG>) <= 8);
+
+  // Addresses are a base that is the same for the wave plus 32 bits per lane:
+  // one register a lane and no arithmetic per load.
+  const uint8_t* w[kTiles];
+  const TS* sc[kTiles];
+  const uint8_t* a;
+  uint32_t aoff[MT], scoff, lane16;
+  int KS, lane;
+  f32x4 acc[kTiles][MT];
+
+  __device__ __forceinline__ void load_rows(Rows& r, int ks) const {
+    const uint8_t* at = a + static_cast<int64_t>(ks) * 256;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) r.act[m][s] = *reinterpret_cast<const uint4*>(at + aoff[m] + s * 64);
+    }
+  }
+  __device__ __forceinline__ void load_scales(Sc& c, int ks) const {
+#pragma unroll
+    for (int f = 0; f < kTiles; ++f)
+      c.s[f] = *reinterpret_cast<const Scales<TS, SG>*>(
+          reinterpret_cast<const uint8_t*>(sc[f] + static_cast<int64_t>(ks) * (16 * SG)) + scoff);
+  }
+  __device__ __forceinline__ void load(Weights& b, int ks) const {
+#pragma unroll
+    for (int f = 0; f < kTiles; ++f) b.w[f] = moe::load_nt16(w[f] + static_cast<int64_t>(ks) * 1024 + lane16);
+  }
+
+  __device__ __forceinline__ void fold(int f, int m, float s, const f32x4& c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[f][m][i] = fmaf(c[i], s, acc[f][m][i]);
+  }
+
+  __device__ __forceinline__ void stage(const Weights& b, const Sc& sc, const Rows& r) {
+#pragma unroll
+    for (int g = 0; g < SG; ++g) {
+      f32x4 c0[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        c0[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (FMT == MOE_W4_INT4) {
+          const bf16x8 minus24 = as_bf16x8(0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u);
+#pragma unroll
+          for (int s = 0; s < SPG; ++s)
+            c0[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_rows(r.act[m][g * SPG + s]), minus24, c0[m], 0, 0, 0);
+        }
+      }
+      if constexpr (MT == 1) {
+        // the four tiles side by side: four independent chains of products
+        f32x4 c[kTiles] = {c0[0], c0[0], c0[0], c0[0]};
+#pragma unroll
+        for (int s = 0; s < SPG; ++s)
+#pragma unroll
+          for (int f = 0; f < kTiles; ++f)
+            c[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_rows(r.act[0][g * SPG + s]),
+                                                           unpack<FMT>(dword(b.w[f], g * SPG + s)), c[f], 0, 0, 0);
+#pragma unroll
+        for (int f = 0; f < kTiles; ++f) fold(f, 0, sc.s[f].get(g), c[f]);
+      } else {
+#pragma unroll
+        for (int f = 0; f < kTiles; ++f) {
+          f32x4 c[MT];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) c[m] = c0[m];
+#pragma unroll
+          for (int s = 0; s < SPG; ++s) {
+            const bf16x8 v = unpack<FMT>(dword(b.w[f], g * SPG + s));
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+              c[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_rows(r.act[m][g * SPG + s]), v, c[m], 0, 0, 0);
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m) fold(f, m, sc.s[f].get(g), c[m]);
+          __builtin_amdgcn_sched_barrier(0);      // one tile's products at a time
+        }
+      }
+    }
+  }
+
+  // Step U of the unrolled pair: the next stage's loads, then this stage.
+  // Loads return in order, so those that are needed sooner go first.
+  template <int U>
+  __device__ __forceinline__ void step(int ks, int next, Weights (&b)[2], Sc (&c)[2], Rows (&r)[2]) {
+    if (ks >= KS) return;
+    constexpr int N = U ^ 1;
+    if constexpr (!kScalesAhead) load_scales(c[0], ks);
+    if constexpr (!kAhead) load_rows(r[0], ks);
+    if (next < KS) {
+      if constexpr (kScalesAhead) load_scales(c[N], next);
+      if constexpr (kAhead) load_rows(r[N], next);
+    }
+    if (next < KS) load(b[N], next);
+    __builtin_amdgcn_sched_barrier(0);
+    stage(b[U], c[kScalesAhead ? U : 0], r[kAhead ? U : 0]);
+  }
+
+  // The sums of rows row0 .. row0 + rows - 1 (rows <= 16 MT) over the wave's
+  // share of the stages: part, part + split, ...
+  __device__ __forceinline__ void products(const GemvArgs& p, int e, int nb, int part, int64_t row0, int rows) {
+    lane = moe::lane_id();
+    const int n = lane & 15, j = lane >> 4;
+    KS = p.K / 128;
+    lane16 = lane * 16;
+    scoff = n * SG * sizeof(TS);
+#pragma unroll
+    for (int f = 0; f < kTiles; ++f) {
+      // 64 rows of G, or 32 gate rows and the 32 up rows they pair with
+      const int64_t tile = static_cast<int64_t>(e) * (p.N / 16) +
+                           (p.silu ? (f >> 1) * (p.N / 32) + nb * 2 + (f & 1) : nb * 4 + f);
+      w[f] = p.codes + tile * KS * 1024;
+      sc[f] = static_cast<const TS*>(p.scales) + tile * KS * (16 * SG);
+    }
+    a = p.a + row0 * p.K * 2;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      // lanes past the last row read row 0 again; what they compute is not stored
+      const uint32_t r = m * 16 + n < rows ? m * 16 + n : 0;
+      aoff[m] = (r * p.K + j * 8) * 2;
+#pragma unroll
+      for (int f = 0; f < kTiles; ++f) acc[f][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    if (part >= KS) return;
+    Weights b[2];
+    Sc c[2];
+    Rows r[2];
+    if constexpr (kScalesAhead) load_scales(c[0], part);
+    if constexpr (kAhead) load_rows(r[0], part);
+    load(b[0], part);
+    for (int ks = part; ks < KS; ks += 2 * p.split) {
+      step<0>(ks, ks + p.split, b, c, r);
+      step<1>(ks + p.split, ks + 2 * p.split, b, c, r);
+    }
+  }
+
+  // this wave's 16 x 64 sums of activation rows 16 m .. into LDS rows
+  __device__ __forceinline__ void spill(int m, float* rows16) const {
+    const int n = lane & 15, j = lane >> 4;
+#pragma unroll
+    for (int f = 0; f < kTiles; ++f)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rows16[(j * 4 + i) * kRedStride + f * 16 + n] = acc[f][m][i];
+  }
+};
+
+// The same for FP8 rows.  Their scales are per activation row and stage, so
+// weights are the first operand here: a lane then has one activation row and
+// one such scale, and it is the weights' scales that lanes share.
 //
 // Lane 16 j + n holds, of every 16 x 16 result, weight rows 4 j .. 4 j + 3 and
 // activation row n, so all 16 lanes of a row of lanes need the same scales.
 // They share one load: lane n fetches the four scales of tile n & 3 and of the
 // (n >> 2)-th group from here on, and the folds read them by row broadcasts,
 // which are operand modifiers of the multiply-add.
-template <int FMT, bool FP8, typename TS, int SG, int MT> struct Block {
-  static constexpr int ESZ = FP8 ? 1 : 2;
+template <int FMT, typename TS, int SG, int MT> struct BlockFp8 {
   static constexpr int SPG = 4 / SG;            // 32-column steps of a scale group
   static constexpr int CH = 4 / SG;             // stages that one scale load covers
   static constexpr int UN = CH < 2 ? 2 : CH;    // stages of the unrolled loop
@@ -158,7 +353,7 @@ template <int FMT, bool FP8, typename TS, int SG, int MT> struct Block {
   static constexpr bool kAhead = MT == 1;
   static constexpr bool kScalesAhead = kAhead || CH < 4;
   struct Rows {
-    Act<FP8> act[MT][4];
+    uint2 act[MT][4];
     float as[MT];
   };
   struct Buf {                                  // one stage's weights
@@ -176,12 +371,12 @@ template <int FMT, bool FP8, typename TS, int SG, int MT> struct Block {
   f32x4 acc[kTiles][MT];
 
   __device__ __forceinline__ void load_rows(Rows& r, int ks) const {
-    const uint8_t* at = a + static_cast<int64_t>(ks) * (128 * ESZ);
+    const uint8_t* at = a + static_cast<int64_t>(ks) * 128;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) r.act[m][s] = *reinterpret_cast<const Act<FP8>*>(at + aoff[m] + s * 32 * ESZ);
-      if constexpr (FP8) r.as[m] = *reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(as + ks) + asoff[m]);
+      for (int s = 0; s < 4; ++s) r.act[m][s] = *reinterpret_cast<const uint2*>(at + aoff[m] + s * 32);
+      r.as[m] = *reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(as + ks) + asoff[m]);
     }
   }
   __device__ __forceinline__ void load(Buf& b, int ks) const {
@@ -190,19 +385,25 @@ template <int FMT, bool FP8, typename TS, int SG, int MT> struct Block {
   }
   __device__ __forceinline__ f32x4 scales(int ks) const {
     const uint32_t k = min(ks + usub, KS - 1);
-    return load_scales(reinterpret_cast<const TS*>(reinterpret_cast<const uint8_t*>(sc) +
-                                                   (scoff + k * (SG * 16 * static_cast<uint32_t>(sizeof(TS))))));
+    const uint8_t* base = reinterpret_cast<const uint8_t*>(sc);
+    const uint32_t at = scoff + k * (SG * 16 * static_cast<uint32_t>(sizeof(TS)));
+    if constexpr (SG == 1 && sizeof(TS) == 4) return *reinterpret_cast<const f32x4*>(base + at);
+    f32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const TS* one = reinterpret_cast<const TS*>(base + (at + i * SG * static_cast<uint32_t>(sizeof(TS))));
+      if constexpr (sizeof(TS) == 4) v[i] = *one;
+      else v[i] = __uint_as_float(static_cast<uint32_t>(*one) << 16);
+    }
+    return v;
   }
 
   template <int SUB, int G, int F> __device__ __forceinline__ void fold(const f32x4& sc, const Rows& r, int m, const f32x4& c) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float s = row_bcast<(SUB * SG + G) * 4 + F>(sc[i]);
-      acc[F][m][i] = fmaf(c[i], FP8 ? s * r.as[m] : s, acc[F][m][i]);
+      acc[F][m][i] = fmaf(c[i], s * r.as[m], acc[F][m][i]);
     }
-  }
-  static __device__ __forceinline__ uint32_t dword(const uint4& v, int d) {
-    return d == 0 ? v.x : d == 1 ? v.y : d == 2 ? v.z : v.w;
   }
 
   template <int SUB, int G> __device__ __forceinline__ void group(const f32x4& sc, const Buf& b, const Rows& r) {
@@ -214,7 +415,7 @@ template <int FMT, bool FP8, typename TS, int SG, int MT> struct Block {
         const bf16x8 minus24 = as_bf16x8(0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u);
 #pragma unroll
         for (int s = 0; s < SPG; ++s)
-          c0[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(minus24, act_bf16(r.act[m][G * SPG + s]), c0[m], 0, 0, 0);
+          c0[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(minus24, as_rows(r.act[m][G * SPG + s]), c0[m], 0, 0, 0);
       }
     }
     if constexpr (MT == 1) {
@@ -225,7 +426,7 @@ template <int FMT, bool FP8, typename TS, int SG, int MT> struct Block {
 #pragma unroll
         for (int f = 0; f < kTiles; ++f)
           c[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(unpack<FMT>(dword(b.w[f], G * SPG + s)),
-                                                         act_bf16(r.act[0][G * SPG + s]), c[f], 0, 0, 0);
+                                                         as_rows(r.act[0][G * SPG + s]), c[f], 0, 0, 0);
       fold<SUB, G, 0>(sc, r, 0, c[0]);
       fold<SUB, G, 1>(sc, r, 0, c[1]);
       fold<SUB, G, 2>(sc, r, 0, c[2]);
@@ -238,7 +439,12 @@ template <int FMT, bool FP8, typename TS, int SG, int MT> struct Block {
     }
   }
   template <int SUB, int G, int F>
-  __device__ __forceinline__ void tile(const f32x4& sc, const Buf& b, const Rows& r, const f32x4 (&c0)[MT]) {
+  __device__ __forceinline__ void tile(const f32x4& shared, const Buf& b, const Rows& r, const f32x4 (&c0)[MT]) {
+    f32x4 sc = shared;
+    // The compiler makes a stage's 64 broadcasts of loaded fp32 scales at its
+    // beginning and spills 180 registers, unless they become values of the tile;
+    // bf16 scales, which are converted first, it leaves where they are.
+    if constexpr (sizeof(TS) == 4) asm volatile("" : "+v"(sc[0]), "+v"(sc[1]), "+v"(sc[2]), "+v"(sc[3]));
     f32x4 c[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) c[m] = c0[m];
@@ -247,7 +453,7 @@ template <int FMT, bool FP8, typename TS, int SG, int MT> struct Block {
       const bf16x8 v = unpack<FMT>(dword(b.w[F], G * SPG + s));
 #pragma unroll
       for (int m = 0; m < MT; ++m)
-        c[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, act_bf16(r.act[m][G * SPG + s]), c[m], 0, 0, 0);
+        c[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, as_rows(r.act[m][G * SPG + s]), c[m], 0, 0, 0);
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) fold<SUB, G, F>(sc, r, m, c[m]);
@@ -302,14 +508,14 @@ template <int FMT, bool FP8, typename TS, int SG, int MT> struct Block {
     const int u = n >> 2;
     usub = u / SG;
     sc = static_cast<const TS*>(p.scales) + tile(0) * KS * SG * 16;
-    scoff = static_cast<uint32_t>(((tile(n & 3) - tile(0)) * KS * SG + u % SG) * 16 + j * 4) * sizeof(TS);
-    a = p.a + row0 * p.K * ESZ;
-    if constexpr (FP8) as = p.a_scales + row0 * KS;
+    scoff = static_cast<uint32_t>((tile(n & 3) - tile(0)) * KS * SG * 16 + j * 4 * SG + u % SG) * sizeof(TS);
+    a = p.a + row0 * p.K;
+    as = p.a_scales + row0 * KS;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       // lanes past the last row read row 0 again; what they compute is not stored
       const uint32_t r = m * 16 + n < rows ? m * 16 + n : 0;
-      aoff[m] = (r * p.K + j * 8) * ESZ;
+      aoff[m] = r * p.K + j * 8;
       asoff[m] = r * KS * 4;
 #pragma unroll
       for (int f = 0; f < kTiles; ++f) acc[f][m] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -335,45 +541,53 @@ template <int FMT, bool FP8, typename TS, int SG, int MT> struct Block {
     }
   }
 
-  // The waves' sums through LDS, in wave order, 16 rows at a time, and the
-  // epilogue.  With split 1 a wave only meets itself.
-  __device__ __forceinline__ void store(const GemvArgs& p, int nb, int part, int64_t row0, int rows, float* mine) const {
+  __device__ __forceinline__ void spill(int m, float* rows16) const {
     const int n = lane & 15, j = lane >> 4;
-    const int cols = p.silu ? 32 : 64, quads = cols / 4;
-    const int ldo = p.silu ? p.N / 2 : p.N;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      if (p.split > 1) __syncthreads();
-#pragma unroll
-      for (int f = 0; f < kTiles; ++f)
-        *reinterpret_cast<f32x4*>(mine + (part * 16 + n) * kRedStride + f * 16 + j * 4) = acc[f][m];
-      if (p.split > 1) __syncthreads();
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      for (int i = part * MOE_WAVE + lane; i < 16 * quads; i += p.split * MOE_WAVE) {
-        const int r = i / quads, q = i % quads * 4;
-        if (m * 16 + r >= rows) break;
-        f32x4 v = {0.f, 0.f, 0.f, 0.f}, u = v;
-        for (int s = 0; s < p.split; ++s) {
-          const float* src = mine + (s * 16 + r) * kRedStride + q;
-          v += *reinterpret_cast<const f32x4*>(src);
-          if (p.silu) u += *reinterpret_cast<const f32x4*>(src + 32);
-        }
-        if (p.silu) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = moe::silu(v[k]) * u[k];
-        }
-        const int64_t at = (row0 + m * 16 + r) * ldo + nb * cols + q;
-        if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
-        else
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
-              make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-    }
+    for (int f = 0; f < kTiles; ++f) *reinterpret_cast<f32x4*>(rows16 + n * kRedStride + f * 16 + j * 4) = acc[f][m];
   }
 };
+
+// The waves' sums through LDS, in wave order, 16 rows at a time, and the
+// epilogue.  With split 1 a wave only meets itself.
+template <int MT, typename B>
+__device__ __forceinline__ void store(const B& blk, const GemvArgs& p, int nb, int part, int64_t row0, int rows, float* mine) {
+  const int lane = blk.lane;
+  const int cols = p.silu ? 32 : 64, quads = cols / 4;
+  const int ldo = p.silu ? p.N / 2 : p.N;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    if (p.split > 1) __syncthreads();
+    blk.spill(m, mine + part * 16 * kRedStride);
+    if (p.split > 1) __syncthreads();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    for (int i = part * MOE_WAVE + lane; i < 16 * quads; i += p.split * MOE_WAVE) {
+      const int r = i / quads, q = i % quads * 4;
+      if (m * 16 + r >= rows) break;
+      f32x4 v = {0.f, 0.f, 0.f, 0.f}, u = v;
+      for (int s = 0; s < p.split; ++s) {
+        const float* src = mine + (s * 16 + r) * kRedStride + q;
+        v += *reinterpret_cast<const f32x4*>(src);
+        if (p.silu) u += *reinterpret_cast<const f32x4*>(src + 32);
+      }
+      if (p.silu) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = moe::silu(v[k]) * u[k];
+      }
+      const int64_t at = (row0 + m * 16 + r) * ldo + nb * cols + q;
+      if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+            make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <int FMT, bool FP8, typename TS, int SG, int MT>
+using Block = std::conditional_t<FP8, BlockFp8<FMT, TS, SG, MT>, BlockBf16<FMT, TS, SG, MT>>;
 
 template <int FMT, bool FP8, typename TS, int SG>
 __global__ __launch_bounds__(kMaxWaves * MOE_WAVE, 3) void gemv_w4_kernel(GemvArgs p) {
@@ -394,11 +608,11 @@ __global__ __launch_bounds__(kMaxWaves * MOE_WAVE, 3) void gemv_w4_kernel(GemvAr
     if (m <= 16) {
       Block<FMT, FP8, TS, SG, 1> w;
       w.products(p, e, nb, part, off + r, m);
-      w.store(p, nb, part, off + r, m, mine);
+      store<1>(w, p, nb, part, off + r, m, mine);
     } else {
       Block<FMT, FP8, TS, SG, 2> w;
       w.products(p, e, nb, part, off + r, m);
-      w.store(p, nb, part, off + r, m, mine);
+      store<2>(w, p, nb, part, off + r, m, mine);
     }
   }
 }

@@ -156,7 +156,7 @@ moe_status moe_permute_fp8(const void* x8, const float* x8_scales, int T, int K,
  *          l holds of row l & 15 the columns 32 s + 8 (l >> 4) + 0..7 as its
  *          dword s (INT4: column 2i in bits 4 i + 3 .. 4 i + 6, 2 i + 1 sixteen
  *          bits above, bit 32 being bit 0; E2M1: in column order)
- *   scales [L][N/16][K/128][128/group][16 rows]
+ *   scales [L][N/16][K/128][16 rows][128/group]
  * Limits: N % 128 == 0, K % 128 == 0, N K <= 2^31, K <= 2^24, L <= 1024, group in
  * {32, 64, 128}; codes, codes_packed and scales_packed 16-byte aligned.
  */
