@@ -82,9 +82,16 @@ __device__ __forceinline__ bf16x8 as_bf16x8(uint32_t a, uint32_t b, uint32_t c, 
   return __builtin_bit_cast(bf16x8, v);
 }
 
-template <int FMT> __device__ __forceinline__ bf16x8 unpack(uint32_t v) {
+// The mask of an INT4 code's place in a vector register: an and-or takes one
+// constant from the scalar side only, and would otherwise be two instructions.
+__device__ __forceinline__ uint32_t code_mask() {
+  uint32_t m = 0x00780078u;
+  asm("" : "+v"(m));
+  return m;
+}
+template <int FMT> __device__ __forceinline__ bf16x8 unpack(uint32_t v, uint32_t m) {
   if constexpr (FMT == MOE_W4_INT4) {
-    constexpr uint32_t m = 0x00780078u, o = 0x41804180u;
+    constexpr uint32_t o = 0x41804180u;
     return as_bf16x8((v & m) | o, ((v >> 4) & m) | o, ((v >> 8) & m) | o, (((v >> 12) | (v << 20)) & m) | o);
   } else {
     return as_bf16x8(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, 1.0f, 0)),
@@ -190,7 +197,7 @@ template <int FMT, typename TS, int SG, int MT> struct BlockBf16 {
   const uint8_t* w[kTiles];
   const TS* sc[kTiles];
   const uint8_t* a;
-  uint32_t aoff[MT], scoff, lane16;
+  uint32_t aoff[MT], scoff, lane16, mask;
   int KS, lane;
   f32x4 acc[kTiles][MT];
 
@@ -240,7 +247,7 @@ template <int FMT, typename TS, int SG, int MT> struct BlockBf16 {
 #pragma unroll
           for (int f = 0; f < kTiles; ++f)
             c[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_rows(r.act[0][g * SPG + s]),
-                                                           unpack<FMT>(dword(b.w[f], g * SPG + s)), c[f], 0, 0, 0);
+                                                           unpack<FMT>(dword(b.w[f], g * SPG + s), mask), c[f], 0, 0, 0);
 #pragma unroll
         for (int f = 0; f < kTiles; ++f) fold(f, 0, sc.s[f].get(g), c[f]);
       } else {
@@ -251,7 +258,7 @@ template <int FMT, typename TS, int SG, int MT> struct BlockBf16 {
           for (int m = 0; m < MT; ++m) c[m] = c0[m];
 #pragma unroll
           for (int s = 0; s < SPG; ++s) {
-            const bf16x8 v = unpack<FMT>(dword(b.w[f], g * SPG + s));
+            const bf16x8 v = unpack<FMT>(dword(b.w[f], g * SPG + s), mask);
 #pragma unroll
             for (int m = 0; m < MT; ++m)
               c[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_rows(r.act[m][g * SPG + s]), v, c[m], 0, 0, 0);
@@ -288,6 +295,7 @@ template <int FMT, typename TS, int SG, int MT> struct BlockBf16 {
     const int n = lane & 15, j = lane >> 4;
     KS = p.K / 128;
     lane16 = lane * 16;
+    mask = code_mask();
     scoff = n * SG * sizeof(TS);
 #pragma unroll
     for (int f = 0; f < kTiles; ++f) {
@@ -366,7 +374,7 @@ template <int FMT, typename TS, int SG, int MT> struct BlockFp8 {
   const uint8_t* a;
   const float* as;
   const TS* sc;
-  uint32_t aoff[MT], asoff[MT], scoff, lane16;
+  uint32_t aoff[MT], asoff[MT], scoff, lane16, mask;
   int KS, usub, lane;
   f32x4 acc[kTiles][MT];
 
@@ -425,7 +433,7 @@ template <int FMT, typename TS, int SG, int MT> struct BlockFp8 {
       for (int s = 0; s < SPG; ++s)
 #pragma unroll
         for (int f = 0; f < kTiles; ++f)
-          c[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(unpack<FMT>(dword(b.w[f], G * SPG + s)),
+          c[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(unpack<FMT>(dword(b.w[f], G * SPG + s), mask),
                                                          as_rows(r.act[0][G * SPG + s]), c[f], 0, 0, 0);
       fold<SUB, G, 0>(sc, r, 0, c[0]);
       fold<SUB, G, 1>(sc, r, 0, c[1]);
@@ -450,7 +458,7 @@ template <int FMT, typename TS, int SG, int MT> struct BlockFp8 {
     for (int m = 0; m < MT; ++m) c[m] = c0[m];
 #pragma unroll
     for (int s = 0; s < SPG; ++s) {
-      const bf16x8 v = unpack<FMT>(dword(b.w[F], G * SPG + s));
+      const bf16x8 v = unpack<FMT>(dword(b.w[F], G * SPG + s), mask);
 #pragma unroll
       for (int m = 0; m < MT; ++m)
         c[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, as_rows(r.act[m][G * SPG + s]), c[m], 0, 0, 0);
@@ -505,6 +513,7 @@ template <int FMT, typename TS, int SG, int MT> struct BlockFp8 {
 #pragma unroll
     for (int f = 0; f < kTiles; ++f) w[f] = p.codes + tile(f) * KS * 1024;
     lane16 = lane * 16;
+    mask = code_mask();
     const int u = n >> 2;
     usub = u / SG;
     sc = static_cast<const TS*>(p.scales) + tile(0) * KS * SG * 16;
