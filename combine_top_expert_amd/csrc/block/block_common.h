@@ -1,5 +1,4 @@
-// Shared by the kernels of libmoe_block.so: argument checks and 8-element row
-// chunks in fp32.
+// Shared by the kernels of libmoe_block.so: argument checks and bf16 values.
 #pragma once
 
 #include "moe_block.h"
@@ -7,34 +6,14 @@
 
 namespace moe_block {
 
+// Most tokens of a call: row counters are 32-bit and step past the last row.
+constexpr int kMaxRows = 1 << 30;
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool real_dtype(int d) { return d == MOE_F32 || d == MOE_BF16; }
 
-// Eight neighbouring elements as fp32.  float: two 16-byte accesses, bf16: one.
-__device__ __forceinline__ void load8(const float* p, float* f) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-__device__ __forceinline__ void load8(const uint16_t* p, float* f) {
-  const uint4 r = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return static_cast<uint32_t>(moe::f32_to_bf16(a)) | (static_cast<uint32_t>(moe::f32_to_bf16(b)) << 16);
-}
-__device__ __forceinline__ void store8(float* p, const float* f) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-}
-__device__ __forceinline__ void store8(uint16_t* p, const float* f) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                                            pack_bf16(f[6], f[7]));
 }
 // the value as its storage type holds it
 template <typename T> __device__ __forceinline__ float as_stored(float v);

@@ -93,12 +93,14 @@ __global__ __launch_bounds__(kMaxWaves * 64) void add_rms_norm_kernel(const T* x
   const int64_t base = static_cast<int64_t>(blockIdx.x) * H;
   const int threads = blockDim.x;
   Chunk<T> cx[VPL], cr[VPL];
+  Chunk<TW> cw[VPL];
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
     const int c = (v * threads + threadIdx.x) * 8;
     if (c < H) {
       cx[v].template load<NT>(x + base + c);
       if (residual) cr[v].template load<NT>(residual + base + c);
+      cw[v].template load<false>(weight + c);
     }
   }
   float h[VPL][8];
@@ -128,7 +130,7 @@ __global__ __launch_bounds__(kMaxWaves * 64) void add_rms_norm_kernel(const T* x
     const int c = (v * threads + threadIdx.x) * 8;
     if (c < H) {
       float w[8];
-      load8(weight + c, w);
+      cw[v].get(w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[v][i] = h[v][i] * r * w[i];
       if (y) put<NT>(y + base + c, h[v]);
@@ -243,7 +245,7 @@ __global__ __launch_bounds__(kMaxWaves * 64) void add_rms_norm_bw_kernel(const T
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
     const int c = (v * threads + threadIdx.x) * 8;
-    if (c < H) store8(part + static_cast<int64_t>(blockIdx.x) * H + c, dw[v]);
+    if (c < H) put<false>(part + static_cast<int64_t>(blockIdx.x) * H + c, dw[v]);
   }
 }
 
@@ -338,6 +340,7 @@ template <typename T, typename TW> void bw_pick(const BwArgs& a) {
 }
 
 inline bool norm_sizes(int T, int H) { return T >= 0 && H > 0; }
+inline bool norm_limits(int T, int H) { return H % 8 == 0 && H <= kMaxH && T <= kMaxRows; }
 inline bool good_eps(float eps) { return eps >= 0.f && eps < INFINITY; }
 
 }  // namespace
@@ -348,7 +351,7 @@ extern "C" moe_status moe_add_rms_norm(const void* x, const void* residual, moe_
   MOE_CHECK(norm_sizes(T, H) && good_eps(eps), MOE_ERR_INVALID_ARG);
   MOE_CHECK(moe_host::valid_dtype(x_dt) && moe_host::valid_dtype(w_dt), MOE_ERR_INVALID_ARG);
   MOE_CHECK(real_dtype(x_dt) && real_dtype(w_dt), MOE_ERR_UNSUPPORTED);
-  MOE_CHECK(H % 8 == 0 && H <= kMaxH, MOE_ERR_UNSUPPORTED);
+  MOE_CHECK(norm_limits(T, H), MOE_ERR_UNSUPPORTED);
   MOE_CHECK(h_out || y || y8 || T == 0, MOE_ERR_INVALID_ARG);
   MOE_CHECK(!y8 == !y8_scales, MOE_ERR_INVALID_ARG);
   MOE_CHECK(!y8 || H % 128 == 0, MOE_ERR_UNSUPPORTED);
@@ -369,7 +372,7 @@ extern "C" moe_status moe_add_rms_norm(const void* x, const void* residual, moe_
 }
 
 extern "C" size_t moe_add_rms_norm_backward_workspace_bytes(int T, int H) {
-  if (!norm_sizes(T, H) || H % 8 != 0 || H > kMaxH) return 0;
+  if (!norm_sizes(T, H) || !norm_limits(T, H)) return 0;
   return static_cast<size_t>(bw_blocks(T, H)) * H * sizeof(float);
 }
 
@@ -380,7 +383,7 @@ extern "C" moe_status moe_add_rms_norm_backward(const void* dy, const void* h, c
   MOE_CHECK(norm_sizes(T, H) && good_eps(eps), MOE_ERR_INVALID_ARG);
   MOE_CHECK(moe_host::valid_dtype(dt) && moe_host::valid_dtype(w_dt), MOE_ERR_INVALID_ARG);
   MOE_CHECK(real_dtype(dt) && real_dtype(w_dt), MOE_ERR_UNSUPPORTED);
-  MOE_CHECK(H % 8 == 0 && H <= kMaxH, MOE_ERR_UNSUPPORTED);
+  MOE_CHECK(norm_limits(T, H), MOE_ERR_UNSUPPORTED);
   MOE_CHECK(d_weight && aligned16(d_weight), MOE_ERR_INVALID_ARG);
   const size_t need = moe_add_rms_norm_backward_workspace_bytes(T, H);
   if (T > 0) {

@@ -781,7 +781,7 @@ extern "C" moe_status moe_router_group_topk(const float* logits, const float* bi
   MOE_CHECK(score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID, MOE_ERR_INVALID_ARG);
   MOE_CHECK(n_group >= 1 && n_group <= E && topk_group >= 1 && topk_group <= n_group, MOE_ERR_INVALID_ARG);
   MOE_CHECK(group_top == 1 || group_top == 2, MOE_ERR_INVALID_ARG);
-  MOE_CHECK(E <= kMaxE && K <= kMaxK && n_group <= MOE_WAVE && E % n_group == 0, MOE_ERR_UNSUPPORTED);
+  MOE_CHECK(E <= kMaxE && K <= kMaxK && T <= kMaxRows && n_group <= MOE_WAVE && E % n_group == 0, MOE_ERR_UNSUPPORTED);
   MOE_CHECK(K <= topk_group * (E / n_group), MOE_ERR_INVALID_ARG);
   MOE_CHECK(route_scale == route_scale && fabsf(route_scale) < INFINITY, MOE_ERR_INVALID_ARG);
   if (T == 0) return MOE_OK;
@@ -810,7 +810,7 @@ extern "C" moe_status moe_router_group_topk_backward(const float* logits, const 
                                                      hipStream_t stream) {
   MOE_CHECK(T >= 0 && E >= 1 && K >= 1 && K <= E, MOE_ERR_INVALID_ARG);
   MOE_CHECK(score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID, MOE_ERR_INVALID_ARG);
-  MOE_CHECK(E <= kMaxE && K <= kMaxK, MOE_ERR_UNSUPPORTED);
+  MOE_CHECK(E <= kMaxE && K <= kMaxK && T <= kMaxRows, MOE_ERR_UNSUPPORTED);
   MOE_CHECK(route_scale == route_scale && fabsf(route_scale) < INFINITY, MOE_ERR_INVALID_ARG);
   if (T == 0) return MOE_OK;
   MOE_CHECK(logits && topk_ids && d_weights && d_logits && d_logits != logits, MOE_ERR_INVALID_ARG);

@@ -56,7 +56,7 @@ int moe_block_abi_version(void);
  *   from fp32 with the recipe of moe_permute (rows that moe_permute_fp8 takes)
  * At least one of h_out, y, y8 is given.  eps >= 0 and finite; a row of zeros
  * with eps = 0 gives NaN.
- * Limits: H % 8 == 0, H <= 16384, H % 128 == 0 with y8; x, residual, weight,
+ * Limits: T <= 2^30, H % 8 == 0, H <= 16384, H % 128 == 0 with y8; x, residual, weight,
  * h_out, y and y8 16-byte aligned.
  */
 moe_status moe_add_rms_norm(const void* x, const void* residual, moe_dtype x_dt, const void* weight,
@@ -107,7 +107,7 @@ moe_status moe_add_rms_norm_backward(const void* dy, const void* h, const void* 
  * candidates lie closer than fp32 can tell apart are decided again in fp64.
  *   logits [T,E] fp32; bias [E] fp32 or NULL; topk_ids [T,K] int32,
  *   topk_weights [T,K] fp32.
- * Limits: E <= 1024, 1 <= K <= 32, E % n_group == 0, n_group <= 64,
+ * Limits: T <= 2^30, E <= 1024, 1 <= K <= 32, E % n_group == 0, n_group <= 64,
  * 1 <= topk_group <= n_group, K <= topk_group * (E / n_group).
  */
 moe_status moe_router_group_topk(const float* logits, const float* bias, int T, int E, int K,
@@ -126,7 +126,7 @@ moe_status moe_router_group_topk(const float* logits, const float* bias, int T, 
  *   softmax: d_logits[e] = s_e (ds_e - sum_k ds_k w_k) over the whole row
  * Every element of d_logits is written (0 where nothing arrives).  Ids outside
  * [0, E) are no route; an id that occurs twice counts twice.
- * Limits: E <= 1024, 1 <= K <= 32.
+ * Limits: T <= 2^30, E <= 1024, 1 <= K <= 32.
  */
 moe_status moe_router_group_topk_backward(const float* logits, const int32_t* topk_ids,
                                           const float* d_weights, int T, int E, int K, moe_score score,

@@ -64,7 +64,7 @@ def test_norm_refusals(ep):
         return ep.block_lib.moe_add_rms_norm(P(x), P(res), xdt, P(w), wdt, eps, T, H, P(h), P(y), P(y8), P(sc), None)
     assert call(T=0, x=None, w=None) == OK
     assert call(T=-1) == INVALID and call(H=0) == INVALID
-    assert call(H=252) == UNSUPPORTED and call(H=16392) == UNSUPPORTED
+    assert call(H=252) == UNSUPPORTED and call(H=16392) == UNSUPPORTED and call(T=(1 << 30) + 1) == UNSUPPORTED
     assert call(H=136, y8=512, sc=512) == UNSUPPORTED              # FP8 groups of 128
     assert call(y8=512) == INVALID and call(sc=512) == INVALID     # codes and scales go together
     assert call(h=None, y=None) == INVALID                         # nothing to write
@@ -80,13 +80,13 @@ def test_norm_refusals(ep):
 
 def test_norm_backward_refusals(ep):
     need = ep.moe_add_rms_norm_backward_workspace_bytes
-    assert need(4, 256) > 0 and need(0, 256) == 0 and need(-1, 256) == 0 and need(4, 252) == 0
+    assert need(4, 256) > 0 and need(0, 256) == 0 and need(-1, 256) == 0 and need(4, 252) == 0 and need((1 << 30) + 1, 8) == 0
     assert need(100000, 4096) < 64 << 20                           # bounded for long batches
 
     def call(dy=256, h=256, dh=256, dt=BF16, w=256, wdt=F32, eps=1e-6, T=4, H=256, dx=512, dw=512, ws=256, wsb=1 << 20):
         return ep.block_lib.moe_add_rms_norm_backward(P(dy), P(h), P(dh), dt, P(w), wdt, eps, T, H, P(dx), P(dw), P(ws),
                                                       wsb, None)
-    assert call(H=100) == UNSUPPORTED and call(H=20000) == UNSUPPORTED
+    assert call(H=100) == UNSUPPORTED and call(H=20000) == UNSUPPORTED and call(T=(1 << 30) + 1) == UNSUPPORTED
     assert call(dt=FP8) == UNSUPPORTED and call(wdt=FP8) == UNSUPPORTED and call(dt=-1) == INVALID
     assert call(wsb=need(4, 256) - 1) == WORKSPACE
     assert call(eps=-1.0) == INVALID and call(T=-1) == INVALID
@@ -101,7 +101,7 @@ def test_route_refusals(ep):
     assert call(T=0, lg=None, ids=None, w=None) == OK
     assert call(K=0) == INVALID and call(K=65) == INVALID
     assert call(K=33, n=1, keep=1) == UNSUPPORTED
-    assert call(E=2048, n=1, keep=1) == UNSUPPORTED
+    assert call(E=2048, n=1, keep=1) == UNSUPPORTED and call(T=(1 << 30) + 1) == UNSUPPORTED
     assert call(n=7) == UNSUPPORTED                                # E % n_group
     assert call(n=0) == INVALID and call(n=128) == INVALID and call(keep=9) == INVALID and call(keep=0) == INVALID
     assert call(E=1024, n=128, keep=4) == UNSUPPORTED              # more groups than lanes
@@ -114,6 +114,7 @@ def test_route_refusals(ep):
     def bw(lg=256, ids=256, dw=256, T=4, E=64, K=8, score=1, scale=1.0, dl=512):
         return ep.block_lib.moe_router_group_topk_backward(P(lg), P(ids), P(dw), T, E, K, score, 1, scale, P(dl), None)
     assert bw(T=0, lg=None, ids=None, dw=None, dl=None) == OK
+    assert bw(T=(1 << 30) + 1) == UNSUPPORTED
     assert bw(K=33) == UNSUPPORTED and bw(E=1025) == UNSUPPORTED and bw(K=0) == INVALID and bw(score=-1) == INVALID
     assert bw(dl=256) == INVALID and bw(scale=NAN) == INVALID
     for name in ("lg", "ids", "dw", "dl"):
