@@ -16,6 +16,13 @@
 // Bound by reading the weights.  A workgroup's four waves share 64 weight rows
 // (four 16-row tiles) and split the columns in stages of 128; each streams its
 // share of the packed weights with 1 KB loads, and their sums meet in LDS.
+//
+// Measured on one decode step (128 tokens, about 130 rows for 32 experts), us:
+// gate/up 4096 x 7168 INT4, a scale per 128, FP8 rows (492 MB) 72 to 80, the
+// same loads without the arithmetic 71.6; down 7168 x 2048 E2M1, a scale per
+// 32, bf16 rows (262 MB) 41.7, loads alone 41.1.  E2M1 gate/up with bf16 rows
+// 68, 7.1 TB/s.  4 / 16 / 17 / 32 / 64 rows in every expert, INT4 gate/up: 92 /
+// 105 / 121 / 146 / 288.
 
 #include <type_traits>
 

@@ -10,6 +10,10 @@
 // lane, a DPP wave sum, then the waves' sums through LDS in wave order.  A
 // group of 128 columns is 16 neighbouring lanes, whose amax is an in-row DPP
 // maximum.
+//
+// Bound by memory.  Forward, 8192 x 7168 bf16 with residual to h and FP8 (413
+// MB): 69.4 us, 5.9 TB/s; backward, 16384 x 4096 bf16 with dh (537 MB): 89.0 us
+// and 4.2 for the reduction of d_w, 5.8 TB/s.
 
 #include "block_common.h"
 #include "router_common.h"

@@ -15,6 +15,11 @@
 // rank the groups), an fp32 score is off by at most a few 2^-24 of the row's
 // scores; a row in which two neighbours of the order lie within that of each
 // other is decided again by the same wave in fp64 (route_exact).
+//
+// Bound by vector instructions: 630 a token in a first form with the same
+// layout, 238 in the one for large batches, which takes 30.6 us for 65536 x 256
+// with 4 of 8 groups and K = 8 (71 MB, 11 us of memory time).  The fp64 path is
+// the other part: an earlier build took 38.6 us with it and 22.4 us without.
 
 #include <type_traits>
 
