@@ -710,7 +710,8 @@ extern "C" moe_status moe_grouped_gemv_w4(const void* a, moe_dtype a_dt, const f
             MOE_ERR_INVALID_ARG);
   MOE_CHECK(a_dt != MOE_F32 && real_dtype(s_dt) && real_dtype(out_dt), MOE_ERR_UNSUPPORTED);
   MOE_CHECK(w4_limits(L, N, K, group), MOE_ERR_UNSUPPORTED);
-  MOE_CHECK(static_cast<int64_t>(L) * (N / 64) <= 0x7fffffff, MOE_ERR_UNSUPPORTED);
+  // a launch has L N split lanes, and waves share a block's stages from K = 2048 on
+  MOE_CHECK(static_cast<int64_t>(L) * N * K < 1ll << 39, MOE_ERR_UNSUPPORTED);
   if (rows_cap == 0) return MOE_OK;
   MOE_CHECK(a && codes_packed && scales_packed && counts && offsets && out, MOE_ERR_INVALID_ARG);
   MOE_CHECK(a_dt != MOE_FP8_E4M3 || a_scales, MOE_ERR_INVALID_ARG);

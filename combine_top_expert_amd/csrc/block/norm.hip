@@ -363,16 +363,20 @@ extern "C" moe_status moe_add_rms_norm(const void* x, const void* residual, moe_
   MOE_CHECK(x && weight && (!y || y != h_out), MOE_ERR_INVALID_ARG);
   MOE_CHECK(aligned16(x) && aligned16(residual) && aligned16(weight) && aligned16(h_out) && aligned16(y) && aligned16(y8),
             MOE_ERR_INVALID_ARG);
-  const FwArgs a{x, residual, weight, eps, T, H, h_out, y, static_cast<uint8_t*>(y8), y8_scales, stream};
-  if (x_dt == MOE_BF16) {
-    if (w_dt == MOE_BF16) fw_pick<uint16_t, uint16_t>(a);
-    else fw_pick<uint16_t, float>(a);
-  } else {
-    if (w_dt == MOE_BF16) fw_pick<float, uint16_t>(a);
-    else fw_pick<float, float>(a);
-  }
-  MOE_LAUNCH_CHECK();
-  return MOE_OK;
+  return in_slices(T, kMaxWaves * 64, [&](int64_t t, int rows) {
+    auto at = [&](auto* p, int64_t step) { return p ? p + t * step : p; };
+    const int64_t bytes = static_cast<int64_t>(H) * (x_dt == MOE_BF16 ? 2 : 4);
+    const FwArgs a{at(static_cast<const uint8_t*>(x), bytes), at(static_cast<const uint8_t*>(residual), bytes), weight,
+                   eps, rows, H, at(static_cast<uint8_t*>(h_out), bytes), at(static_cast<uint8_t*>(y), bytes),
+                   at(static_cast<uint8_t*>(y8), H), at(y8_scales, H / 128), stream};
+    if (x_dt == MOE_BF16) {
+      if (w_dt == MOE_BF16) fw_pick<uint16_t, uint16_t>(a);
+      else fw_pick<uint16_t, float>(a);
+    } else {
+      if (w_dt == MOE_BF16) fw_pick<float, uint16_t>(a);
+      else fw_pick<float, float>(a);
+    }
+  });
 }
 
 extern "C" size_t moe_add_rms_norm_backward_workspace_bytes(int T, int H) {

@@ -63,10 +63,10 @@ extern "C" moe_status moe_permute_fp8(const void* x8, const float* x8_scales, in
   MOE_CHECK(moe_block::aligned16(x8) && moe_block::aligned16(buf), MOE_ERR_INVALID_ARG);
   const int parts = (H / 16 + kChunks - 1) / kChunks;
   const int64_t grid = static_cast<int64_t>(T) * parts;
-  MOE_CHECK(grid <= 0x7fffffff, MOE_ERR_UNSUPPORTED);
-  permute_fp8_kernel<<<static_cast<int>(grid), MOE_WAVE, 0, stream>>>(
-      static_cast<const uint8_t*>(x8), x8_scales, T, K, H, slot_of, rows_cap, static_cast<uint8_t*>(buf), buf_scales,
-      parts);
-  MOE_LAUNCH_CHECK();
-  return MOE_OK;
+  MOE_CHECK(grid <= 0x7fffffff && parts <= 1 << 14, MOE_ERR_UNSUPPORTED);
+  return moe_block::in_slices(T, static_cast<int64_t>(parts) * MOE_WAVE, [&](int64_t t, int rows) {
+    permute_fp8_kernel<<<rows * parts, MOE_WAVE, 0, stream>>>(
+        static_cast<const uint8_t*>(x8) + t * H, x8_scales + t * (H / 128), rows, K, H, slot_of + t * K, rows_cap,
+        static_cast<uint8_t*>(buf), buf_scales, parts);
+  });
 }

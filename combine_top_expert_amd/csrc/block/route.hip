@@ -791,22 +791,26 @@ extern "C" moe_status moe_router_group_topk(const float* logits, const float* bi
   MOE_CHECK(route_scale == route_scale && fabsf(route_scale) < INFINITY, MOE_ERR_INVALID_ARG);
   if (T == 0) return MOE_OK;
   MOE_CHECK(logits && topk_ids && topk_weights, MOE_ERR_INVALID_ARG);
-  const RouteArgs a{logits, bias, T, E, K, score == MOE_SCORE_SIGMOID, n_group, topk_group, group_top, E / n_group,
-                    renorm ? 1 : 0, route_scale, 0, topk_ids, topk_weights};
+  RouteArgs a{logits, bias, T, E, K, score == MOE_SCORE_SIGMOID, n_group, topk_group, group_top, E / n_group,
+              renorm ? 1 : 0, route_scale, 0, topk_ids, topk_weights};
   // Four tokens a wave from 5120 tokens on, where they fill the card: wave per
   // token against four tokens a wave, us, E = 256, K = 8, 4 of 8 groups: 128
   // tokens 4.5 / 5.9, 2048: 8.5 / 9.4, 4096: 9.6 / 9.5, 8192: 13.7 / 12.0, 65536:
   // 58 / 32; E = 128, K = 6: 4096: 6.6 / 6.9, 8192: 8.9 / 7.6, 65536: 41 / 20.
   constexpr int kSegFrom = 5120;
-  if (T >= kSegFrom && E > 128 && E <= 256 && seg_fits<16>(a)) launch_seg<16>(a, stream);
-  else if (T >= kSegFrom && E > 64 && E <= 128 && seg_fits<8>(a)) launch_seg<8>(a, stream);
-  else if (E <= 64) launch_fw<1>(a, stream);
-  else if (E <= 128) launch_fw<2>(a, stream);
-  else if (E <= 256) launch_fw<4>(a, stream);
-  else if (E <= 512) launch_fw<8>(a, stream);
-  else launch_fw<16>(a, stream);
-  MOE_LAUNCH_CHECK();
-  return MOE_OK;
+  return in_slices(T, MOE_WAVE, [&](int64_t t, int rows) {
+    a.logits = logits + t * E;
+    a.T = rows;
+    a.ids = topk_ids + t * K;
+    a.weights = topk_weights + t * K;
+    if (T >= kSegFrom && E > 128 && E <= 256 && seg_fits<16>(a)) launch_seg<16>(a, stream);
+    else if (T >= kSegFrom && E > 64 && E <= 128 && seg_fits<8>(a)) launch_seg<8>(a, stream);
+    else if (E <= 64) launch_fw<1>(a, stream);
+    else if (E <= 128) launch_fw<2>(a, stream);
+    else if (E <= 256) launch_fw<4>(a, stream);
+    else if (E <= 512) launch_fw<8>(a, stream);
+    else launch_fw<16>(a, stream);
+  });
 }
 
 extern "C" moe_status moe_router_group_topk_backward(const float* logits, const int32_t* topk_ids,
@@ -820,19 +824,21 @@ extern "C" moe_status moe_router_group_topk_backward(const float* logits, const 
   if (T == 0) return MOE_OK;
   MOE_CHECK(logits && topk_ids && d_weights && d_logits && d_logits != logits, MOE_ERR_INVALID_ARG);
   RouteArgs a{};
-  a.logits = logits;
-  a.T = T;
   a.E = E;
   a.K = K;
   a.sigmoid = score == MOE_SCORE_SIGMOID;
   a.renorm = renorm ? 1 : 0;
   a.scale = route_scale;
-  a.ids = const_cast<int32_t*>(topk_ids);
-  if (E <= 64) launch_bw<1>(a, d_weights, d_logits, stream);
-  else if (E <= 128) launch_bw<2>(a, d_weights, d_logits, stream);
-  else if (E <= 256) launch_bw<4>(a, d_weights, d_logits, stream);
-  else if (E <= 512) launch_bw<8>(a, d_weights, d_logits, stream);
-  else launch_bw<16>(a, d_weights, d_logits, stream);
-  MOE_LAUNCH_CHECK();
-  return MOE_OK;
+  return in_slices(T, MOE_WAVE / 2, [&](int64_t t, int rows) {
+    a.logits = logits + t * E;
+    a.T = rows;
+    a.ids = const_cast<int32_t*>(topk_ids) + t * K;
+    const float* dw = d_weights + t * K;
+    float* dl = d_logits + t * E;
+    if (E <= 64) launch_bw<1>(a, dw, dl, stream);
+    else if (E <= 128) launch_bw<2>(a, dw, dl, stream);
+    else if (E <= 256) launch_bw<4>(a, dw, dl, stream);
+    else if (E <= 512) launch_bw<8>(a, dw, dl, stream);
+    else launch_bw<16>(a, dw, dl, stream);
+  });
 }

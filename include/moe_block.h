@@ -139,7 +139,8 @@ moe_status moe_router_group_topk_backward(const float* logits, const int32_t* to
  * for every (t,k) with 0 <= slot_of < rows_cap, copied bit for bit.
  *   x8 [T,H] e4m3fn, x8_scales [T,H/128] fp32 (as moe_add_rms_norm writes
  *   them); slot_of [T,K]; buf [rows_cap,H], buf_scales [rows_cap,H/128]
- * Limits: H % 128 == 0, K <= 64; x8, buf 16-byte aligned.
+ * Limits: H % 128 == 0, H <= 2^25, K <= 64, T times the 2 KB parts of a row below
+ * 2^31; x8, buf 16-byte aligned.
  */
 moe_status moe_permute_fp8(const void* x8, const float* x8_scales, int T, int K, int H,
                            const int32_t* slot_of, int64_t rows_cap, void* buf, float* buf_scales,
@@ -181,9 +182,10 @@ moe_status moe_pack_w4(const void* codes, const void* scales, moe_dtype s_dt, mo
  *   out_dt in {F32, BF16}
  * Every count is right; weights are read once per 32 rows of an expert, so this
  * is the form for few rows per expert (moe_grouped_gemm_w13 / _w2 for many).
- * An infinite or NaN activation makes its row NaN.
- * Limits: N % 128 == 0, K % 128 == 0, N K <= 2^31, K <= 2^24, L <= 1024, group in
- * {32, 64, 128}; a, codes_packed, scales_packed and out 16-byte aligned.
+ * An infinite or NaN activation makes its row NaN; so may, with INT4 codes, finite
+ * ones whose sums over a group pass 2^123 (codes ride as 16 + code).
+ * Limits: N % 128 == 0, K % 128 == 0, N K <= 2^31, L N K < 2^39, K <= 2^24,
+ * L <= 1024, group in {32, 64, 128}; a, codes_packed, scales_packed and out 16-byte aligned.
  */
 moe_status moe_grouped_gemv_w4(const void* a, moe_dtype a_dt, const float* a_scales,
                                const void* codes_packed, const void* scales_packed, moe_dtype s_dt,
