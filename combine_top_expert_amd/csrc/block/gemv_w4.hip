@@ -3,13 +3,13 @@
 //
 // G[q,n] = sum_g scale[n,g] sum_{k in g} A[q,k] value(code[n,k]).  The 4-bit
 // values are exact in bf16 and go to the bf16 matrix cores (16 weight rows x 32
-// columns), with up to 16 activation rows as the other operand.  Each scale group starts from a fresh accumulator, whose
-// result is folded into fp32 sums with its scales.
+// columns), with up to 16 activation rows as the other operand.  Each scale
+// group starts from a fresh accumulator, whose result is folded into fp32 sums
+// with its scales.
 //
 // INT4 codes become 16 + code by placing the nibble in the mantissa of 16.0
-// (7 instructions for 8 values); a product with the constant -24
-// over the same columns, shared by all of a wave's weight tiles, takes the
-// offset off.  16 is the smallest offset that keeps a nibble in one binade,
+// (7 instructions for 8 values); a product with the constant -24 over the same
+// columns, shared by all of a wave's weight tiles, takes the offset off.  16 is the smallest offset that keeps a nibble in one binade,
 // and keeps the cancelled part within about six times a group's own terms.
 // E2M1 codes are converted by the hardware, two per instruction.
 //
