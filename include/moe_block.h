@@ -53,9 +53,13 @@ int moe_block_abi_version(void);
  *   h_out [T,H] x_dt, or NULL; may be x or residual itself (in place)
  *   y [T,H] x_dt, or NULL; may be x or residual itself, not h_out
  *   y8 [T,H] e4m3fn with y8_scales [T,H/128] fp32, or both NULL: y quantised
- *   from fp32 with the recipe of moe_permute (rows that moe_permute_fp8 takes)
+ *   from fp32 with the recipe of moe_permute (rows that moe_permute_fp8 takes);
+ *   where a group's y holds a NaN its scale and codes are NaN, and one whose
+ *   largest magnitude is infinite has scale infinity, code NaN at its infinities
+ *   and 0 elsewhere, so that no broken row leaves as numbers
  * At least one of h_out, y, y8 is given.  eps >= 0 and finite; a row of zeros
- * with eps = 0 gives NaN.
+ * with eps = 0 gives NaN, in y and in y8.  The mean square is fp32's: a row
+ * whose squares pass fp32's range has r = 0.
  * Limits: T <= 2^30, H % 8 == 0, H <= 16384, H % 128 == 0 with y8; x, residual, weight,
  * h_out, y and y8 16-byte aligned.
  */
