@@ -10,11 +10,12 @@
 // lane's list.  Lanes are in expert order and the sort is stable, so equal keys
 // go to the lower id.
 //
-// The order is the one of exact scores.  Without a bias it is the logits' order,
-// which needs no arithmetic.  Where arithmetic decides (a bias, or the sums that
-// rank the groups), an fp32 score is off by at most a few 2^-24 of the row's
-// scores; a row in which two neighbours of the order lie within that of each
-// other is decided again by the same wave in fp64 (route_exact).
+// The order is the one of fp64 scores.  Without a bias it is the logits' order,
+// which needs no arithmetic, as long as fp64 tells the scores apart (may_tie).
+// Where arithmetic decides (a bias, or the sums that rank the groups), an fp32
+// score is off by at most a few 2^-24 of the row's scores.  A row in which two
+// neighbours of the order may tie, or lie within that of each other, is decided
+// again by the same wave in fp64 (route_exact).
 //
 // Bound by vector instructions: 630 a token in a first form with the same
 // layout, 238 in the one for large batches, which takes 30.6 us for 65536 x 256
@@ -301,6 +302,21 @@ __global__ __launch_bounds__(kThreads) void group_topk_kernel(RouteArgs a) {
   // reciprocal), for softmax by the sum's and the quotient's roundings too
   // (NPL + 6 additions, terms that are off by 5 kU on average at most).
   const float c0 = SIG ? 6.f : 20.f + NPL;
+
+  // Whether logits v > o may have the same fp64 score.  Neighbouring fp32 logits
+  // have different ones, but for sigmoid from 23 on, where 1 + exp(-l) is rounded
+  // to steps of 2^-52 (from 37 on all are 1), where the score underflows (-708
+  // below the largest, with sigmoid below 0), and next to 0, where logits lie
+  // closer than fp64 can tell 1 + l (or l less the largest) apart.
+  auto may_tie = [&](float v, float o) {
+    return v > o && (v - o < 1e-12f || (SIG ? o > 20.f || v < -700.f : v - m < -700.f));
+  };
+  // whether it can hold at all: of two logits, both below 2^-15 (1e-12 apart
+  // means that), or outside an ordinary range
+  auto two_in_zone = [&](bool live, float v) {
+    const bool in = fabsf(v) < 0x1p-15f || (SIG ? fabsf(v) > 20.f : v - m < -700.f);
+    return __popcll(__ballot(live && in)) > 1;
+  };
   uint32_t key[NPL];
   int id[NPL];
   float err = 0.f, all = 0.f;
@@ -363,7 +379,11 @@ __global__ __launch_bounds__(kThreads) void group_topk_kernel(RouteArgs a) {
     }
     // the group's score; dead groups keep key 0
     uint32_t gkey = 0;
-    if (t1 && g < a.n_group) {
+    bool look = true;                                   // at the edge between the groups that stay and the others
+    if (!BIAS && a.group_top == 1) {
+      gkey = g < a.n_group ? t1 : 0u;
+      look = two_in_zone(gkey > 1, key_value(gkey));
+    } else if (t1 && g < a.n_group) {
       float v = key_value(t1);
       if (a.group_top == 2) {
         if (!BIAS) v = fast_score(v);
@@ -381,14 +401,15 @@ __global__ __launch_bounds__(kThreads) void group_topk_kernel(RouteArgs a) {
     // the last group that stays and the first that does not
     const uint64_t in = __ballot(g < a.n_group && rank == a.topk_group - 1);
     const uint64_t out = __ballot(g < a.n_group && rank == a.topk_group);
-    if (out && (BIAS || a.group_top == 2)) {
+    if (out && look) {
       const uint32_t ki = __builtin_amdgcn_readlane(gkey, __builtin_ctzll(in));
       const uint32_t ko = __builtin_amdgcn_readlane(gkey, __builtin_ctzll(out));
       if (ki > 1 && ko > 1) {
         const float vi = key_value(ki), vo = key_value(ko);
         // without a bias a sum of two scores is off by its own share
         // (exponents to 88) and by what fp32 loses below its normal range
-        near = vi - vo <= (BIAS ? 4.f * tol + 2.f * kU * (fabsf(vi) + fabsf(vo)) : (c0 + 140.f) * kU * (vi + vo) + 1e-37f);
+        near = BIAS ? vi - vo <= 4.f * tol + 2.f * kU * (fabsf(vi) + fabsf(vo))
+               : a.group_top == 2 ? vi - vo <= (c0 + 140.f) * kU * (vi + vo) + 1e-37f : may_tie(vi, vo);
       }
     }
     if (runs) {
@@ -427,18 +448,31 @@ __global__ __launch_bounds__(kThreads) void group_topk_kernel(RouteArgs a) {
       near = __ballot(lane < a.K && mine > 1 && next > 1 && key_value(mine) - key_value(next) <= 2.f * tol) != 0;
     }
   }
-  if (near) my = route_exact<NPL, SIG, BIAS>(a, row, lds + static_cast<size_t>(wave) * a.E, lane);
 
-  // lane k's logit, from the lane that holds it
-  float x = 0.f;
-  if constexpr (NPL <= 4) {
-    const int from = max(my, 0) / NPL;
-    each<NPL>([&](auto j) {
-      const float v = __shfl(l[j], from);
-      x = max(my, 0) % NPL == j ? v : x;
-    });
-  } else {
-    x = row[max(my, 0)];
+  // lane k's logit, from the lane that holds it (lane K: the runner-up's)
+  auto logit = [&]() {
+    float v = 0.f;
+    if constexpr (NPL <= 4) {
+      const int from = max(my, 0) / NPL;
+      each<NPL>([&](auto j) {
+        const float o = __shfl(l[j], from);
+        v = max(my, 0) % NPL == j ? o : v;
+      });
+    } else {
+      v = row[max(my, 0)];
+    }
+    return v;
+  };
+  float x = logit();
+  if (!BIAS && !near) {
+    if (two_in_zone(my >= 0, x)) {
+      const float o = __shfl_down(x, 1);
+      near = __ballot(lane < a.K && __shfl_down(my, 1) >= 0 && may_tie(x, o)) != 0;
+    }
+  }
+  if (near) {
+    my = route_exact<NPL, SIG, BIAS>(a, row, lds + static_cast<size_t>(wave) * a.E, lane);
+    x = logit();
   }
   const bool real = lane < a.K && my >= 0;
   float w = real ? (SIG ? sigmoid_f(x) : expf(x - m) / sum) : 0.f;

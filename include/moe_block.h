@@ -107,8 +107,11 @@ moe_status moe_add_rms_norm_backward(const void* dy, const void* h, const void* 
  * are -1 ("no route" to moe_dispatch_layout) with weight 0: a fully masked row
  * (a padded token) routes nowhere.  A NaN score ranks below every number and
  * above a masked expert.
- * Scores are fp32, but the choice is the one that exact scores give: rows whose
- * candidates lie closer than fp32 can tell apart are decided again in fp64.
+ * Scores are fp32, but the choice is the one that fp64 scores give, with and
+ * without a bias: rows whose candidates lie closer than fp32 can tell apart are
+ * decided again in fp64.  Scores that are the same fp64 number tie, as those of
+ * sigmoid logits above 37 (all 1) or of logits more than 746 below the largest
+ * with softmax (all 0).
  *   logits [T,E] fp32; bias [E] fp32 or NULL; topk_ids [T,K] int32,
  *   topk_weights [T,K] fp32.
  * Limits: T <= 2^30, E <= 1024, 1 <= K <= 32, E % n_group == 0, n_group <= 64,

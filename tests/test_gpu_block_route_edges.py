@@ -1,0 +1,83 @@
+"""Routing at the edges of its scores' range."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import announce, need_gpu
+from oracle import block as ob
+
+pytestmark = pytest.mark.gpu
+U = ob.U
+
+
+@pytest.fixture(scope="module")
+def ep():
+    need_gpu()
+    import combine_top_expert_amd as ep
+    return ep
+
+
+def route(ep, logits, K, bias=None, score="sigmoid", n=1, keep=1, top=2, renorm=True):
+    T = logits.shape[0]
+    ids = torch.full((T, K), -9, dtype=torch.int32, device="cuda")
+    w = torch.full((T, K), math.nan, device="cuda")
+    ep.moe_router_group_topk(torch.from_numpy(logits).cuda(), K, ids, w,
+                             bias=None if bias is None else torch.from_numpy(bias).cuda(),
+                             score=ep.MOE_SCORE_SIGMOID if score == "sigmoid" else ep.MOE_SCORE_SOFTMAX, n_group=n,
+                             topk_group=keep, group_top=top, renorm=renorm)
+    torch.cuda.synchronize()
+    return ids.cpu().numpy(), w.double().cpu().numpy()
+
+
+def same_choice(ep, rows, K, T=None, **kw):
+    """The oracle's ids for `rows`, repeated to a batch of T."""
+    at = np.arange(len(rows)) if T is None else np.resize(np.arange(len(rows)), T)
+    want, _ = ob.group_topk(rows, K, kw.get("bias"), kw.get("score", "sigmoid"), kw.get("n", 1), kw.get("keep", 1),
+                            kw.get("top", 2))
+    ids, _ = route(ep, rows[at], K, **kw)
+    assert np.array_equal(ids, want[at]), (kw, np.argwhere(ids != want[at])[:4].tolist())
+    return want
+
+
+def saturated_rows(E, rng):
+    """Sigmoid logits whose fp64 scores tie (from about 37 on all are 1, from 23
+    on neighbouring logits' are), ordinary ones among them, and tiny logits."""
+    step = np.float32(2.0 ** -19)                       # neighbouring logits between 16 and 32
+    up = (24 + step * rng.permutation(E)).astype(np.float32)
+    rows = [np.arange(40, 40 + E), np.arange(40 + E, 40, -1), up, up + 6, 1e-20 * rng.permutation(E),
+            15 + 30 * rng.random(E), np.where(rng.random(E) < 0.5, 50 * rng.random(E), rng.standard_normal(E)),
+            -1000.0 - rng.permutation(E), np.where(np.arange(E) % 2, 0.0, -1000.0 - rng.permutation(E))]
+    rows = np.stack(rows).astype(np.float32)
+    rows[5, 1], rows[6, 0] = np.inf, np.inf
+    return rows
+
+
+@pytest.mark.parametrize("E,K,n,keep", [(8, 2, 1, 1), (8, 2, 2, 1), (8, 3, 4, 2), (64, 6, 1, 1), (100, 7, 5, 2), (256, 8, 1, 1),
+                                        (256, 8, 8, 4), (384, 12, 2, 1), (1024, 32, 1, 1), (1024, 32, 64, 16)])
+def test_route_saturated_sigmoid(ep, E, K, n, keep):
+    """One rule with and without groups and bias: scores that fp64 does not tell
+    apart tie, and ties go to the lower id."""
+    announce("route saturated", E, K, n, keep)
+    rng = np.random.default_rng(E + n)
+    rows = saturated_rows(E, rng)
+    for bias in (None, np.zeros(E, np.float32)):
+        for top in (1, 2):
+            want = same_choice(ep, rows, K, bias=bias, n=n, keep=keep, top=top)
+    if n == 1:
+        assert want[0].tolist() == list(range(K))
+
+
+@pytest.mark.parametrize("E,K,n,keep", [(8, 2, 1, 1), (8, 2, 2, 1), (64, 6, 1, 1), (100, 7, 5, 2), (256, 8, 8, 4), (1024, 32, 1, 1)])
+def test_route_softmax_ties(ep, E, K, n, keep):
+    """Softmax scores that fp64 does not tell apart: logits that differ by less
+    than its step, and those whose scores underflow."""
+    announce("route softmax ties", E, K, n, keep)
+    rng = np.random.default_rng(E + n)
+    rows = np.stack([1e-20 * rng.permutation(E), np.where(np.arange(E) < 2, 3.0, 1e-18 * rng.permutation(E)),
+                     np.where(np.arange(E) % 4, -1000.0 - rng.permutation(E), 0.0),
+                     np.where(np.arange(E) == 3, 1.0, -2000.0 + rng.permutation(E))]).astype(np.float32)
+    for bias in (None, np.zeros(E, np.float32)):
+        for top in (1, 2):
+            same_choice(ep, rows, K, score="softmax", bias=bias, n=n, keep=keep, top=top)
