@@ -588,9 +588,11 @@ __global__ __launch_bounds__(kThreads) void group_topk_seg_kernel(RouteArgs a) {
   bool near = ((odd >> (seg * kSeg)) & 0xffffu) != 0;
   // How far a c may be off, its own rounding aside: fast_exp's share of s grows
   // with the exponent, but s |l| is at most smax |lmax| + 1.3 smax (sigmoid), and
-  // exp(-d) d at most 0.37 (softmax, plus the sum's NPL + 4 additions).
+  // exp(-d) d at most 0.37 (softmax, plus the sum's NPL + 4 additions).  |lmax| is
+  // cut where sigmoid is 0 or 1 to fp32: far below, smax is 0 and the product has
+  // to stay a number.
   const float smax = SIG ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-lmax)) : inv;
-  const float tol = smax * (SIG ? 8.f + 1.5f * fabsf(lmax) : 20.f + NPL) * kU;
+  const float tol = smax * (SIG ? 8.f + 1.5f * fminf(fabsf(lmax), 128.f) : 20.f + NPL) * kU;
 
   bool kept = true;
   if (a.n_group > 1) {

@@ -81,3 +81,17 @@ def test_route_softmax_ties(ep, E, K, n, keep):
     for bias in (None, np.zeros(E, np.float32)):
         for top in (1, 2):
             same_choice(ep, rows, K, score="softmax", bias=bias, n=n, keep=keep, top=top)
+
+
+@pytest.mark.parametrize("E,K,n,keep", [(256, 8, 1, 1), (256, 8, 8, 4), (128, 6, 4, 2), (160, 6, 1, 1)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_rows_far_below_every_score(ep, E, K, n, keep, score):
+    """Rows filled with a large negative number that is no mask, biases that tie:
+    the lower ids, in large batches as in small ones."""
+    announce("route far below", E, K, n, keep, score)
+    rng = np.random.default_rng(E)
+    rows = np.stack([np.full(E, -3e38), np.full(E, -2.5e38), np.where(rng.random(E) < 0.5, -3e38, -np.inf),
+                     rng.standard_normal(E), np.full(E, 3e38)]).astype(np.float32)
+    for bias in (np.zeros(E, np.float32), (np.round(rng.standard_normal(E)) / 4).astype(np.float32)):
+        for T in (None, 5123):
+            same_choice(ep, rows, K, T, bias=bias, score=score, n=n, keep=keep)
