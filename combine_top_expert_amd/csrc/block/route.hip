@@ -611,12 +611,13 @@ __global__ __launch_bounds__(kThreads) void group_topk_seg_kernel(RouteArgs a) {
     int rank = 0;
     for (int h = 0; h < a.n_group; ++h) rank += __shfl(gs, h * lg, kSeg) > gs ? 1 : 0;
     kept = !dead && rank < a.topk_group;
-    // the worst group that stays against the best that does not; equal scores
-    // share a rank, so a tie at the edge keeps too many
+    // the worst group that stays against the best live one that does not, if
+    // there is one; equal scores share a rank, so a tie at the edge keeps too many
     const float vi = -moe_router::row_max_f32(kept ? -gs : -INFINITY);
     const float vo = moe_router::row_max_f32(kept ? -INFINITY : gs);
     const uint32_t lanes = static_cast<uint32_t>(__ballot(kept && used) >> (seg * kSeg)) & 0xffffu;
-    near |= vi - vo <= 4.f * tol + 4.f * kU * (fabsf(vi) + fabsf(vo)) || __popc(lanes) > a.topk_group * lg;
+    near |= (vo > -INFINITY && vi - vo <= 4.f * tol + 4.f * kU * (fabsf(vi) + fabsf(vo))) ||
+            __popc(lanes) > a.topk_group * lg;
   }
 
   uint32_t key[NPL];

@@ -95,3 +95,53 @@ def test_route_rows_far_below_every_score(ep, E, K, n, keep, score):
     for bias in (np.zeros(E, np.float32), (np.round(rng.standard_normal(E)) / 4).astype(np.float32)):
         for T in (None, 5123):
             same_choice(ep, rows, K, T, bias=bias, score=score, n=n, keep=keep)
+
+
+def call_time(fn, calls=20, rounds=5):
+    """Microseconds a call, the best of some rounds."""
+    best = math.inf
+    for _ in range(rounds):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(calls):
+            fn()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3 / calls)
+    return best
+
+
+def test_route_batches_that_drop_no_live_group(ep):
+    """A batch in which every group stays, or in which the dropped groups are all
+    masked, or whose rows are padding, costs about what any other does: its
+    rows are not decided in fp64."""
+    announce("route keeps every live group")
+    T, E, K = 65536, 256, 8
+    torch.manual_seed(4)
+    logits, bias = torch.randn(T, E, device="cuda"), 0.1 * torch.randn(E, device="cuda")
+    half = logits.clone()
+    half[:, 128:] = -math.inf                            # four of eight groups masked
+    none = torch.full_like(logits, -math.inf)
+    ids, w = torch.empty(T, K, dtype=torch.int32, device="cuda"), torch.empty(T, K, device="cuda")
+
+    def time(x, keep, score):
+        return call_time(lambda: ep.moe_router_group_topk(x, K, ids, w, bias=bias, n_group=8, topk_group=keep, score=score))
+    for score in (ep.MOE_SCORE_SIGMOID, ep.MOE_SCORE_SOFTMAX):
+        usual = time(logits, 4, score)
+        others = {"all stay": time(logits, 8, score), "others masked": time(half, 4, score), "all masked": time(none, 4, score)}
+        print(f"[metric] score {score}: 4 of 8 {usual:.1f} us, " + ", ".join(f"{k} {v:.1f}" for k, v in others.items()))
+        assert max(others.values()) < 1.75 * usual
+
+
+@pytest.mark.parametrize("E,K,n,keep", [(256, 8, 8, 8), (128, 6, 4, 4), (160, 6, 5, 5), (256, 8, 8, 6)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_choice_where_no_live_group_is_dropped(ep, E, K, n, keep, score):
+    announce("route no live group dropped", E, K, n, keep, score)
+    rng = np.random.default_rng(E + keep)
+    x = rng.standard_normal((40, E)).astype(np.float32)
+    x[30:, (E // n) * (keep // 2):] = -np.inf            # fewer live groups than stay
+    x[20:30, rng.random(E) < 0.5] = -np.inf
+    x[38:] = -np.inf
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
+    for top in (1, 2):
+        same_choice(ep, x, K, 5123, bias=bias, score=score, n=n, keep=keep, top=top)
