@@ -40,6 +40,9 @@ constexpr int kMaxE = 1024;
 constexpr int kMaxK = 32;
 constexpr float kMask = -3.3e38f;   // covers -inf and the lowest finite fp32 and bf16
 constexpr float kU = 5.9604644775390625e-8f;   // 2^-24, half a step of fp32
+// An exponential or reciprocal below 2^-126 = 1.2e-38 is flushed to 0, which a
+// relative error does not cover: eight of those.
+constexpr float kFlush = 1e-37f;
 
 // f(0), f(1), ... f(N - 1) with constant arguments: arrays indexed so stay in
 // single registers (a loop that is unrolled later makes the compiler hold
@@ -339,7 +342,7 @@ __global__ __launch_bounds__(kThreads) void group_topk_kernel(RouteArgs a) {
     }
   });
   // how far a c may be off: 0 without a bias, where keys are exact
-  const float tol = BIAS ? wave_max_f32(err) * kU : 0.f;
+  const float tol = BIAS ? wave_max_f32(err) * kU + kFlush : 0.f;
 
   bool near = BIAS && __ballot(all != all) != 0;       // a NaN among the scores
   if (a.n_group > 1 && !near) {
@@ -409,7 +412,7 @@ __global__ __launch_bounds__(kThreads) void group_topk_kernel(RouteArgs a) {
         // without a bias a sum of two scores is off by its own share
         // (exponents to 88) and by what fp32 loses below its normal range
         near = BIAS ? vi - vo <= 4.f * tol + 2.f * kU * (fabsf(vi) + fabsf(vo))
-               : a.group_top == 2 ? vi - vo <= (c0 + 140.f) * kU * (vi + vo) + 1e-37f : may_tie(vi, vo);
+               : a.group_top == 2 ? vi - vo <= (c0 + 140.f) * kU * (vi + vo) + kFlush : may_tie(vi, vo);
       }
     }
     if (runs) {
@@ -592,7 +595,7 @@ __global__ __launch_bounds__(kThreads) void group_topk_seg_kernel(RouteArgs a) {
   // cut where sigmoid is 0 or 1 to fp32: far below, smax is 0 and the product has
   // to stay a number.
   const float smax = SIG ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-lmax)) : inv;
-  const float tol = smax * (SIG ? 8.f + 1.5f * fminf(fabsf(lmax), 128.f) : 20.f + NPL) * kU;
+  const float tol = smax * (SIG ? 8.f + 1.5f * fminf(fabsf(lmax), 128.f) : 20.f + NPL) * kU + kFlush;
 
   bool kept = true;
   if (a.n_group > 1) {

@@ -97,6 +97,22 @@ def test_route_rows_far_below_every_score(ep, E, K, n, keep, score):
             same_choice(ep, rows, K, T, bias=bias, score=score, n=n, keep=keep)
 
 
+@pytest.mark.parametrize("E,T", [(8, None), (256, None), (256, 5123)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("n", [1, 2])
+def test_route_scores_below_fp32s_normal_range(ep, E, T, score, n):
+    """Scores that fp32 hardware flushes to zero, against biases of their size."""
+    announce("route tiny scores", E, T, score, n)
+    row, bias = np.full(E, -200.0, np.float32), np.zeros(E, np.float32)
+    row[E - 3] = -87.5                                   # sigmoid 1.0e-38, below 2^-126
+    bias[1] = 5e-39
+    if score == "softmax":
+        row[0] = 0.0                                     # its own score is 1 and leaves through the bias
+        bias[0] = -2.0
+    want = same_choice(ep, row[None], 1, T, score=score, bias=bias, n=n, keep=1, top=1)
+    assert want[0, 0] == E - 3
+
+
 def call_time(fn, calls=20, rounds=5):
     """Microseconds a call, the best of some rounds."""
     best = math.inf
