@@ -696,13 +696,42 @@ template <int SEG> __device__ __forceinline__ double seg_sum_f64(double v) {
   return v;
 }
 
+
+// a + b where each holds partial sums of its own token in all lanes: afterwards
+// the lower half of the lanes (ROW16: of every 32 lanes) holds a's, the upper b's.
+template <bool ROW16> __device__ __forceinline__ double halves_f64(double a, double b) {
+  const int64_t u = __double_as_longlong(a), v = __double_as_longlong(b);
+  auto swap = [](uint32_t x, uint32_t y) {
+    if constexpr (ROW16) return __builtin_amdgcn_permlane16_swap(x, y, false, false);
+    else return __builtin_amdgcn_permlane32_swap(x, y, false, false);
+  };
+  const auto lo = swap(static_cast<uint32_t>(u), static_cast<uint32_t>(v));
+  const auto hi = swap(static_cast<uint32_t>(u >> 32), static_cast<uint32_t>(v >> 32));
+  auto join = [](uint32_t h, uint32_t l) {
+    return __longlong_as_double(static_cast<int64_t>((static_cast<uint64_t>(h) << 32) | l));
+  };
+  return join(hi[0], lo[0]) + join(hi[1], lo[1]);
+}
+
+// Whether a rotation of a 16-lane row of v meets `other` in this lane: by 1 to 8,
+// which brings every two lanes of the row together once, or by 1 to 15.
+template <int SEG, int R = 1> __device__ __forceinline__ bool twice(int v, int other) {
+  bool same = other == __builtin_amdgcn_update_dpp(0, v, 0x120 + R, 0xF, 0xF, true);
+  if constexpr (R < (SEG == 32 ? 15 : 8)) same |= twice<SEG, R + 1>(v, other);
+  return same;
+}
+
 // Backward: a wave takes 64 / SEG tokens.  The routes' part is computed for all
 // of them at once, route k of token i in lane i SEG + k; then the wave writes
-// the rows one after the other: 0 (sigmoid) or the softmax's -s_e dot, plus what
-// the routes add.  The routes' part is in fp64: with renormalised weights the
-// terms of ds cancel (all of them for K = 1, and the softmax's sum_k ds_k w_k
-// vanishes).  With one token a wave that part, in which 6 or 8 of 64 lanes
-// work, bound the kernel (8192 x 256, K = 8: 6.9 us).
+// the rows one after the other: 0 (sigmoid) or the softmax's -s_e dot, and at the
+// routes' experts what they computed.  The routes' part is in fp64, an expert
+// that occurs twice included: with renormalised weights the terms of ds cancel
+// (all of them for K = 1, and the softmax's sum_k ds_k w_k vanishes), and so do
+// ds_e and that sum where an expert has nearly all of the softmax.  For that 1 - s
+// has to hold, so a row's exponentials, fp32 each, are added in fp64, and a
+// route's score is the quotient of the very same two.  With one token a wave the
+// routes' part, in which 6 or 8 of 64 lanes work, bound the kernel (8192 x 256,
+// K = 8: 6.9 us).
 template <int NPL, bool SIG, int SEG>
 __global__ __launch_bounds__(kThreads) void group_topk_bw_kernel(RouteArgs a, const float* __restrict__ d_weights,
                                                                  float* __restrict__ d_logits) {
@@ -712,27 +741,32 @@ __global__ __launch_bounds__(kThreads) void group_topk_bw_kernel(RouteArgs a, co
   const int t0 = (blockIdx.x * kWaves + (threadIdx.x >> 6)) * kTok;
   if (t0 >= a.T) return;
   const int e0 = lane * NPL;
-  float p[kTok][NPL];
-  float m = 0.f, sum = 1.f;                     // of this lane's own token
+  float p[kTok][NPL];                           // the exponentials
+  float m = 0.f;                                // of this lane's own token, as what follows
+  double inv = 1.0;
   if constexpr (!SIG) {
     each<kTok>([&](auto i) {
       const float* row = a.logits + static_cast<int64_t>(min(t0 + i, a.T - 1)) * a.E;
       each<NPL>([&](auto j) { p[i][j] = e0 + j < a.E ? row[e0 + j] : -INFINITY; });
     });
+    double part[kTok];
     each<kTok>([&](auto i) {
-      float mi = -INFINITY, si = 0.f;
+      float mi = -INFINITY;
+      part[i] = 0.0;
       each<NPL>([&](auto j) { mi = p[i][j] <= kMask ? mi : fmaxf(mi, p[i][j]); });
       mi = wave_max_f32(mi);
       each<NPL>([&](auto j) {
         p[i][j] = p[i][j] <= kMask ? 0.f : expf(p[i][j] - mi);
-        si += p[i][j];
+        part[i] += static_cast<double>(p[i][j]);
       });
-      si = wave_sum_f32(si);
-      const float inv = si == 0.f ? 0.f : 1.0f / si;
-      each<NPL>([&](auto j) { p[i][j] *= inv; });
       m = seg == i ? mi : m;
-      sum = seg == i ? si : sum;
     });
+    // every token's sum into its own lanes
+    double sum;
+    if constexpr (kTok == 4) sum = halves_f64<true>(halves_f64<false>(part[0], part[2]), halves_f64<false>(part[1], part[3]));
+    else sum = halves_f64<false>(part[0], part[1]);
+    sum = seg_sum_f64<SEG>(sum);
+    inv = sum == 0.0 ? 0.0 : 1.0 / sum;
   }
   const int t = t0 + seg;
   const bool on = t < a.T && sl < a.K;
@@ -741,7 +775,7 @@ __global__ __launch_bounds__(kThreads) void group_topk_bw_kernel(RouteArgs a, co
   double s = 0.0, d = 0.0;
   if (id >= 0) {
     const float x = a.logits[static_cast<int64_t>(t) * a.E + id];
-    if (!(x <= kMask)) s = SIG ? 1.0 / (1.0 + exp(-static_cast<double>(x))) : static_cast<double>(expf(x - m) / sum);
+    if (!(x <= kMask)) s = SIG ? 1.0 / (1.0 + exp(-static_cast<double>(x))) : static_cast<double>(expf(x - m)) * inv;
     d = static_cast<double>(d_weights[static_cast<int64_t>(t) * a.K + sl]) * static_cast<double>(a.scale);
   }
   if (a.renorm) {
@@ -750,18 +784,37 @@ __global__ __launch_bounds__(kThreads) void group_topk_bw_kernel(RouteArgs a, co
     const double mean = seg_sum_f64<SEG>(d * s) / S;
     d = id >= 0 ? (d - mean) / S : 0.0;
   }
-  // g: what route k adds to its expert's element
-  const float dot = SIG ? 0.f : static_cast<float>(seg_sum_f64<SEG>(d * s));
-  const float g = static_cast<float>(SIG ? d * s * (1.0 - s) : d * s);
+  const double dot = SIG ? 0.0 : seg_sum_f64<SEG>(d * s);
+  // g: the element of route k's expert; of routes to the same one the first has it
+  const int name = id >= 0 ? id : -1 - sl;
+  bool same = twice<16>(name, name);
+  if constexpr (SEG == 32) {
+    const int other = __shfl_xor(name, 16);
+    same |= name == other || twice<32>(name, other);
+  }
+  if (__ballot(same)) {
+    double all = 0.0;
+    bool later = false;
+    for (int k = 0; k < a.K; ++k) {
+      const int other = __shfl(id, k, SEG);
+      const double dk = __shfl(d, k, SEG);
+      all += other == id ? dk : 0.0;
+      later |= other == id && k < sl;
+    }
+    d = all;
+    if (later) id = -1;
+  }
+  const float g = static_cast<float>(SIG ? d * s * (1.0 - s) : s * (d - dot));
+  const float rest = static_cast<float>(-dot * inv);          // times its exponential: the other experts' elements
   each<kTok>([&](auto i) {
     if (t0 + i >= a.T) return;
     float o[NPL];
-    const float di = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(dot), i * SEG));
-    each<NPL>([&](auto j) { o[j] = SIG ? 0.f : -p[i][j] * di; });
+    const float ci = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(rest), i * SEG));
+    each<NPL>([&](auto j) { o[j] = SIG ? 0.f : p[i][j] * ci; });
     for (int k = 0; k < a.K; ++k) {
       const int e = __builtin_amdgcn_readlane(id, i * SEG + k);
       const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g), i * SEG + k));
-      each<NPL>([&](auto j) { o[j] += e == e0 + j ? v : 0.f; });
+      each<NPL>([&](auto j) { o[j] = e == e0 + j ? v : o[j]; });
     }
     float* out = d_logits + static_cast<int64_t>(t0 + i) * a.E;
     if (NPL % 4 == 0 && a.vec) {

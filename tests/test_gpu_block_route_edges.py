@@ -161,3 +161,80 @@ def test_route_choice_where_no_live_group_is_dropped(ep, E, K, n, keep, score):
     bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
     for top in (1, 2):
         same_choice(ep, x, K, 5123, bias=bias, score=score, n=n, keep=keep, top=top)
+
+
+def backward(ep, x, ids, dw, score, scale=1.0):
+    dl = torch.full(x.shape, math.nan, device="cuda")
+    ep.moe_router_group_topk_backward(torch.from_numpy(x).cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(dw).cuda(), dl,
+                                      score=score, renorm=False, route_scale=scale)
+    torch.cuda.synchronize()
+    return dl.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("E", [8, 64, 100, 256, 1000])
+@pytest.mark.parametrize("K", [1, 2, 20])
+def test_softmax_gradient_of_confident_routers(ep, E, K):
+    """One expert holds all but e^-gap of a row: ds_e - sum_k ds_k s_k loses all
+    but that much of its terms.
+
+    Each exponential is off by at most (spread + 3) u of itself (l - max and the
+    exponential), so a score and what is left of 1 beside it are within twice
+    that, and s_e (ds_e (1 - s_e) - sum over the others of ds_k s_k) within four
+    times that of the sum of its terms; four roundings to fp32 and those of
+    fp64 (2^-49 of the uncancelled terms) come on top."""
+    if K > E:
+        pytest.skip("K > E")
+    announce("softmax gradient, confident", E, K)
+    rng = np.random.default_rng(E + K)
+    gaps = np.array([4, 8, 10, 12, 14, 16], np.float32)
+    x = (0.3 * rng.standard_normal((30, E))).astype(np.float32)
+    top = rng.integers(0, E, 30)
+    x[np.arange(30), top] += np.resize(gaps, 30) + math.log(E)
+    ids = np.stack([np.concatenate([[t], rng.permutation(np.delete(np.arange(E), t))[:K - 1]]) for t in top]).astype(np.int32)
+    dw = (0.5 + rng.random((30, K))).astype(np.float32)
+    dw[:6] = 1.0
+    if K > 1:
+        ids[7, 1] = ids[7, 0]                            # twice, and the two all but cancel
+        dw[7, 1] = -dw[7, 0] * np.float32(1 - 2.0 ** -10)
+        ids[8, K - 1] = -1
+    got = backward(ep, x, ids, dw, ep.MOE_SCORE_SOFTMAX, 2.5)
+    worst = 0.0
+    for t in range(30):
+        e = np.exp(x[t].astype(np.float64) - x[t].max())
+        s = e / math.fsum(e)
+        d = np.zeros(E)
+        for k in range(K):
+            if ids[t, k] >= 0:
+                d[ids[t, k]] += 2.5 * float(dw[t, k])
+        rest = np.array([math.fsum(np.delete(e, i)) for i in range(E)]) / math.fsum(e)      # 1 - s
+        cross = np.array([math.fsum(np.delete(d * s, i)) for i in range(E)])
+        ref = s * (d * rest - cross)
+        size = s * (np.abs(d) * rest + math.fsum(np.abs(d * s)) - np.abs(d * s))
+        spread = float(x[t].max() - x[t].min())
+        bound = (4 * (spread + 3) + 4) * U * size + 2.0 ** -49 * s * (np.abs(d) + np.abs(d * s).sum()) + 1e-40
+        worst = max(worst, float(np.max(np.abs(got[t] - ref) / bound)))
+        assert np.all(np.abs(got[t] - ref) <= bound), (t, np.max(np.abs(got[t] - ref) / bound))
+    print(f"[metric] softmax gradient {E} {K}: worst error / bound {worst:.3f}")
+
+
+@pytest.mark.parametrize("K", [2, 8, 15, 16, 17, 20, 32])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_gradient_where_an_expert_occurs_twice(ep, K, score):
+    """At every two places of a token's ids, at three, and at all."""
+    announce("gradient, expert twice", K, score)
+    E = 40
+    rng = np.random.default_rng(K)
+    pairs = [(i, j) for i in range(K) for j in range(i)] + [()]
+    T = len(pairs) + 3
+    x = rng.standard_normal((T, E)).astype(np.float32)
+    ids = np.stack([rng.permutation(E)[:K] for _ in range(T)]).astype(np.int32)
+    for t, at in enumerate(pairs):
+        if at:
+            ids[t, at[0]] = ids[t, at[1]]
+    ids[T - 3, [0, K // 2, K - 1]] = 5
+    ids[T - 2] = 7
+    ids[T - 1, ::2] = -1                                     # no route is no expert that occurs twice
+    dw = rng.standard_normal((T, K)).astype(np.float32)
+    ref, mag = ob.group_topk_backward(x, ids, dw, score, False, 2.5)
+    got = backward(ep, x, ids, dw, ep.MOE_SCORE_SIGMOID if score == "sigmoid" else ep.MOE_SCORE_SOFTMAX, 2.5)
+    assert np.all(np.abs(got - ref) <= 160 * U * mag + 1e-30), np.argwhere(np.abs(got - ref) > 160 * U * mag + 1e-30)[:4].tolist()
