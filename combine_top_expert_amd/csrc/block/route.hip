@@ -772,10 +772,18 @@ __global__ __launch_bounds__(kThreads) void group_topk_bw_kernel(RouteArgs a, co
   const bool on = t < a.T && sl < a.K;
   int id = on ? a.ids[static_cast<int64_t>(t) * a.K + sl] : -1;
   if (id >= a.E) id = -1;
-  double s = 0.0, d = 0.0;
+  double s = 0.0, d = 0.0, off = 1.0;             // the score, its gradient and, for sigmoid, 1 - s
   if (id >= 0) {
     const float x = a.logits[static_cast<int64_t>(t) * a.E + id];
-    if (!(x <= kMask)) s = SIG ? 1.0 / (1.0 + exp(-static_cast<double>(x))) : static_cast<double>(expf(x - m)) * inv;
+    if (!(x <= kMask)) {
+      if constexpr (SIG) {
+        const double e = exp(-fabs(static_cast<double>(x))), r = 1.0 / (1.0 + e);
+        s = x < 0.f ? e * r : r;
+        off = x < 0.f ? r : e * r;
+      } else {
+        s = static_cast<double>(expf(x - m)) * inv;
+      }
+    }
     d = static_cast<double>(d_weights[static_cast<int64_t>(t) * a.K + sl]) * static_cast<double>(a.scale);
   }
   if (a.renorm) {
@@ -804,7 +812,7 @@ __global__ __launch_bounds__(kThreads) void group_topk_bw_kernel(RouteArgs a, co
     d = all;
     if (later) id = -1;
   }
-  const float g = static_cast<float>(SIG ? d * s * (1.0 - s) : s * (d - dot));
+  const float g = static_cast<float>(SIG ? d * s * off : s * (d - dot));
   const float rest = static_cast<float>(-dot * inv);          // times its exponential: the other experts' elements
   each<kTok>([&](auto i) {
     if (t0 + i >= a.T) return;

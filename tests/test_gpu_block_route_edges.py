@@ -238,3 +238,20 @@ def test_gradient_where_an_expert_occurs_twice(ep, K, score):
     ref, mag = ob.group_topk_backward(x, ids, dw, score, False, 2.5)
     got = backward(ep, x, ids, dw, ep.MOE_SCORE_SIGMOID if score == "sigmoid" else ep.MOE_SCORE_SOFTMAX, 2.5)
     assert np.all(np.abs(got - ref) <= 160 * U * mag + 1e-30), np.argwhere(np.abs(got - ref) > 160 * U * mag + 1e-30)[:4].tolist()
+
+
+@pytest.mark.parametrize("E", [8, 256])
+def test_sigmoid_gradient_of_saturated_logits(ep, E):
+    """s (1 - s) keeps its digits where s is 1 to fp64: formed in fp64 from one
+    exponential, rounded once."""
+    announce("sigmoid gradient, saturated", E)
+    x = np.resize(np.array([-80, -40, -20, -1, 0, 1, 17, 20, 25, 30, 36, 40, 60, 80], np.float32), (14, E)).astype(np.float32)
+    ids = np.stack([np.full(14, 3), np.full(14, 5)], 1).astype(np.int32)
+    x[:, 3] = np.array([-80, -40, -20, -1, 0, 1, 17, 20, 25, 30, 36, 40, 60, 80], np.float32)
+    dw = np.linspace(0.5, 2.0, 28).reshape(14, 2).astype(np.float32)
+    got = backward(ep, x, ids, dw, ep.MOE_SCORE_SIGMOID)
+    for t in range(14):
+        for k in range(2):
+            v = float(x[t, ids[t, k]])
+            ref = float(dw[t, k]) / (1 + math.exp(-v)) / (1 + math.exp(v))
+            assert abs(got[t, ids[t, k]] - ref) <= (2.0 ** -24 + 2.0 ** -45) * ref + 1e-45, (v, got[t, ids[t, k]], ref)
