@@ -111,6 +111,15 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: _stream(torch.empty(0, device=torch.device("cuda", dev))))
 
 
+_INT_MAX, _UNSUPPORTED = 0x7fffffff, -2
+
+
+def _too_large(fn: str):
+    """A size that the C ABI's int does not hold (ctypes would cut it off and
+    the call work on what is left)."""
+    raise MoEError(fn, _UNSUPPORTED)
+
+
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _CALL = {name: getattr(block_lib, name) for name in _SIG}
 
@@ -136,6 +145,8 @@ def moe_add_rms_norm(x, residual, weight, eps, h_out=None, y=None, y8=None, y8_s
     norm times weight [H], y8/y8_scales = y in block FP8 (any of the three may
     be None).  h_out or y may be x or residual itself."""
     T, H = rows = x.shape
+    if T > _INT_MAX or H > _INT_MAX:
+        _too_large("moe_add_rms_norm")
     dt = (x.dtype,) if x.dtype in _REAL else _REAL
     if y8 is not None or y8_scales is not None:
         _need(y8_scales, "y8_scales", True)
@@ -149,6 +160,8 @@ def moe_add_rms_norm(x, residual, weight, eps, h_out=None, y=None, y8=None, y8_s
 
 
 def moe_add_rms_norm_backward_workspace_bytes(T: int, H: int) -> int:
+    if max(T, H) > _INT_MAX or min(T, H) < 0:
+        return 0
     return int(block_lib.moe_add_rms_norm_backward_workspace_bytes(T, H))
 
 
@@ -157,6 +170,8 @@ def moe_add_rms_norm_backward(dy, h, weight, eps, dx, d_weight, workspace, dh=No
     dx [T,H], the gradient of x and of residual, and d_weight [H] fp32.
     workspace: moe_add_rms_norm_backward_workspace_bytes(T, H) bytes or more."""
     T, H = rows = dy.shape
+    if T > _INT_MAX or H > _INT_MAX:
+        _too_large("moe_add_rms_norm_backward")
     dt = (dy.dtype,) if dy.dtype in _REAL else _REAL
     dev, (pdy, ph, pdh, pw, pdx, pdw, pws) = _pointers(
         ("dy", dy, dt, rows), ("h", h, dt, rows), ("dh", dh, dt, rows), ("weight", weight, _REAL, (H,)),
@@ -174,6 +189,8 @@ def moe_router_group_topk(logits, K, topk_ids, topk_weights, bias=None, score=MO
     """logits [T,E] fp32 (+ bias [E] fp32, for the choice only) -> topk_ids
     [T,K] int32 (-1 where no expert remains), topk_weights [T,K] fp32."""
     T, E = rows = logits.shape
+    if max(T, E, K, n_group, topk_group) > _INT_MAX:
+        _too_large("moe_router_group_topk")
     dev, (pl, pb, pi, pw) = _pointers(
         ("logits", logits, _F32, rows), ("bias", bias, _F32, (E,)), ("topk_ids", topk_ids, _I32, (T, K)),
         ("topk_weights", topk_weights, _F32, (T, K)))
@@ -188,6 +205,8 @@ def moe_router_group_topk_backward(logits, topk_ids, d_weights, d_logits, score=
     and topk_ids [T,K] -> d_logits [T,E] fp32, every element written."""
     T, E = rows = logits.shape
     K = topk_ids.shape[1]
+    if max(T, E, K) > _INT_MAX:
+        _too_large("moe_router_group_topk_backward")
     dev, (pl, pi, pdw, pdl) = _pointers(
         ("logits", logits, _F32, rows), ("topk_ids", topk_ids, _I32, (T, K)),
         ("d_weights", d_weights, _F32, (T, K)), ("d_logits", d_logits, _F32, rows))
@@ -202,6 +221,8 @@ def moe_permute_fp8(x8, x8_scales, slot_of, buf, buf_scales, bind=False):
     [rows_cap,H], buf_scales [rows_cap,H/128], copied bit for bit."""
     T, H = x8.shape
     K, cap = slot_of.shape[1], buf.shape[0]
+    if max(T, H, K) > _INT_MAX:
+        _too_large("moe_permute_fp8")
     dev, (px, pxs, psl, pb, pbs) = _pointers(
         ("x8", x8, _FP8, (T, H)), ("x8_scales", x8_scales, _F32, (T, H // 128)), ("slot_of", slot_of, _I32, (T, K)),
         ("buf", buf, _FP8, (cap, H)), ("buf_scales", buf_scales, _F32, (cap, H // 128)))
@@ -221,6 +242,8 @@ def moe_pack_w4(codes, scales, fmt, codes_packed, scales_packed, bind=False):
     scales [L,N,K/group] (fp32|bf16) -> the same in the order that
     moe_grouped_gemv_w4 reads (same shapes and dtypes)."""
     L, N, half = codes.shape
+    if max(L, N, 2 * half) > _INT_MAX:
+        _too_large("moe_pack_w4")
     group = _group(2 * half, scales, "scales")
     dt = (scales.dtype,) if scales.dtype in _REAL else _REAL
     per = (L, N, 2 * half // group)
@@ -237,6 +260,8 @@ def moe_grouped_gemv_w4(a, a_scales, codes_packed, scales_packed, fmt, counts, o
     [rows_cap,N/2] = SiLU(gate) * up (fp32|bf16), on valid rows only."""
     L, N, half = codes_packed.shape
     rows_cap, K = a.shape[0], 2 * half
+    if max(L, N, K) > _INT_MAX:
+        _too_large("moe_grouped_gemv_w4")
     group = _group(K, scales_packed, "scales_packed")
     fp8 = a.dtype in _FP8
     _need(a_scales, "a_scales", fp8)
