@@ -29,10 +29,22 @@ BLOCK_LIB_PATH = Path(os.environ.get("MOE_BLOCK_LIB", Path(__file__).resolve().p
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_W4_INT4, MOE_W4_E2M1 = 0, 1
 
-if not BLOCK_LIB_PATH.exists():
-    raise ImportError(f"{BLOCK_LIB_PATH} is not built; run `python combine_top_expert_amd/build.py` "
-                      "(these operators have no fallback without their HIP library)")
-block_lib = ctypes.CDLL(str(BLOCK_LIB_PATH))
+
+class _NotBuilt:
+    """In the library's place where it is missing: a program that uses the share
+    only (libmoe_ep.so) needs none of it, and one that calls into it is told."""
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name}: {BLOCK_LIB_PATH} is not built; run `python combine_top_expert_amd/build.py` "
+                          "(these operators have no fallback without their HIP library)")
+
+
+if BLOCK_LIB_PATH.exists():
+    block_lib = ctypes.CDLL(str(BLOCK_LIB_PATH))
+elif "MOE_BLOCK_LIB" in os.environ:                  # asked for by name
+    raise ImportError(f"MOE_BLOCK_LIB={BLOCK_LIB_PATH} is not built")
+else:
+    block_lib = _NotBuilt()
 
 _p, _i, _i64, _sz, _fl = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _SIG = {
@@ -46,7 +58,7 @@ _SIG = {
     "moe_pack_w4": (_i, [_p, _p, _i, _i, _i, _i, _i, _i, _p, _p, _p]),
     "moe_grouped_gemv_w4": (_i, [_p, _i, _p, _p, _p, _i, _i, _i, _p, _p, _i, _i64, _i, _i, _i, _p, _i, _p]),
 }
-for _name, (_res, _args) in _SIG.items():
+for _name, (_res, _args) in _SIG.items() if BLOCK_LIB_PATH.exists() else ():
     if not hasattr(block_lib, _name):
         raise ImportError(f"{BLOCK_LIB_PATH} lacks {_name}: it predates these sources; rebuild with "
                           "`python combine_top_expert_amd/build.py`")
@@ -121,7 +133,17 @@ def _too_large(fn: str):
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-_CALL = {name: getattr(block_lib, name) for name in _SIG}
+
+
+class _Calls(dict):
+    """The entry points, looked up in the library once."""
+
+    def __missing__(self, name):
+        self[name] = getattr(block_lib, name)
+        return self[name]
+
+
+_CALL = _Calls()
 
 
 def _run(fn: str, bind: bool, dev: int, args: tuple):
