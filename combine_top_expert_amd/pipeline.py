@@ -122,11 +122,16 @@ class MoELayer:
         byte), the scales [L,2I,H/group] and [L,H,I/group] (fp32 or bf16);
         both are packed (moe_pack_w4), and only the packed copies are kept."""
         if self.shape.wdt in _W4:
-            self.w4 = []
+            if w13_scales is None or w2_scales is None:
+                raise ValueError("w13_scales and w2_scales are required for 4-bit weights")
+            held, pack = [], []
             for codes, scales in ((w13, w13_scales), (w2, w2_scales)):
                 packed = torch.empty_like(codes), torch.empty_like(scales)
-                moe_pack_w4(codes, scales, _W4[self.shape.wdt], *packed)
-                self.w4.append(packed)
+                pack.append(moe_pack_w4(codes, scales, _W4[self.shape.wdt], *packed, bind=True))
+                held.append(packed)
+            for f in pack:                                   # both were checked before either is written
+                f()
+            self.w4 = held
             return
         self.w13, self.w2, self.w13_scales, self.w2_scales = w13, w2, w13_scales, w2_scales
         self.w13_packed = None
