@@ -120,13 +120,19 @@ class MoELayer:
 
         4-bit layers: w13 [L,2I,H/2] and w2 [L,H,I/2] are codes (uint8, two a
         byte), the scales [L,2I,H/group] and [L,H,I/group] (fp32 or bf16);
-        both are packed (moe_pack_w4), and only the packed copies are kept."""
+        both are packed (moe_pack_w4), and only the packed copies are kept.
+        New weights of the same sizes and dtypes are packed over the old copies,
+        so bound and captured steps read them; with another scale group or
+        scale dtype such steps have to be bound and captured again, as with
+        every other weight type."""
         if self.shape.wdt in _W4:
             if w13_scales is None or w2_scales is None:
                 raise ValueError("w13_scales and w2_scales are required for 4-bit weights")
             held, pack = [], []
-            for codes, scales in ((w13, w13_scales), (w2, w2_scales)):
-                packed = torch.empty_like(codes), torch.empty_like(scales)
+            for i, (codes, scales) in enumerate(((w13, w13_scales), (w2, w2_scales))):
+                old = self.w4[i] if self.w4 is not None else (None, None)
+                packed = tuple(o if o is not None and (o.shape, o.dtype, o.device) == (t.shape, t.dtype, t.device)
+                               else torch.empty_like(t) for o, t in zip(old, (codes, scales)))
                 pack.append(moe_pack_w4(codes, scales, _W4[self.shape.wdt], *packed, bind=True))
                 held.append(packed)
             for f in pack:                                   # both were checked before either is written
@@ -278,7 +284,9 @@ class MoELayer:
         """The forward's launches as (name, callable) pairs, each marshalled
         once (shapes checked, pointers and the current stream looked up), so
         calling them runs the path with a few microseconds of host time per
-        launch.  The tensors must stay alive and unchanged in shape."""
+        launch.  The tensors must stay alive and unchanged in shape, and the
+        weights be those of the last set_weights (4-bit weights: or later ones
+        of the same sizes)."""
         s = self.shape
         st = [
             ("layout", moe_dispatch_layout(topk_ids, s.E, s.expert_begin, s.L, s.R, s.BM, self.counts,
