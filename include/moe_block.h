@@ -189,8 +189,9 @@ moe_status moe_pack_w4(const void* codes, const void* scales, moe_dtype s_dt, mo
  *   out_dt in {F32, BF16}
  * Every count is right; weights are read once per 32 rows of an expert, so this
  * is the form for few rows per expert (moe_grouped_gemm_w13 / _w2 for many).
- * An infinite or NaN activation makes its row NaN; so may, with INT4 codes, finite
- * ones whose sums over a group pass 2^123 (codes ride as 16 + code).
+ * A row with an infinite or NaN activation (or scale of it) has no finite value:
+ * with INT4 codes and bf16 rows it is NaN, as may be finite rows whose sums over a
+ * group pass 2^123 (codes ride as 16 + code).  Other rows are not touched by it.
  * Limits: N % 128 == 0, K % 128 == 0, N K <= 2^31, L N K < 2^39, K <= 2^24,
  * L <= 1024, group in {32, 64, 128}; a, codes_packed, scales_packed and out 16-byte aligned.
  */
