@@ -9,8 +9,9 @@
 //
 // INT4 codes become 16 + code by placing the nibble in the mantissa of 16.0
 // (7 instructions for 8 values); a product with the constant -24 over the same
-// columns, shared by all of a wave's weight tiles, takes the offset off.  16 is the smallest offset that keeps a nibble in one binade,
-// and keeps the cancelled part within about six times a group's own terms.
+// columns, shared by all of a wave's weight tiles, takes the offset off.  16 is
+// the smallest offset that keeps a nibble in one binade, and keeps the cancelled
+// part within about six times a group's own terms.
 // E2M1 codes are converted by the hardware, two per instruction.
 //
 // Bound by reading the weights.  A workgroup's four waves share 64 weight rows
@@ -20,9 +21,12 @@
 // Measured on one decode step (128 tokens, about 130 rows for 32 experts), us:
 // gate/up 4096 x 7168 INT4, a scale per 128, FP8 rows (492 MB) 72 to 80, the
 // same loads without the arithmetic 71.6; down 7168 x 2048 E2M1, a scale per
-// 32, bf16 rows (262 MB) 41.7, loads alone 41.1.  E2M1 gate/up with bf16 rows
-// 68, 7.1 TB/s.  4 / 16 / 17 / 32 / 64 rows in every expert, INT4 gate/up: 92 /
-// 105 / 121 / 146 / 288.
+// 32, bf16 rows (262 MB) 41.8 to 43.4, loads alone 41.1.  The same number of rows
+// in every expert, 1 / 4 / 16 / 17 / 32 / 64 / 256: INT4 gate/up, FP8 rows 84 / 83 /
+// 102 / 121 / 155 / 305 / 1203; bf16 rows 75 / 77 / 99 / 113 / 140 / 272 / 1088; E2M1
+// gate/up, a scale per 128, FP8 rows 79 / 80 / 100 / 116 / 153 / 299 / 1178; per 32, bf16
+// rows 81 / 84 / 105 / 119 / 148 / 291 / 1140; down 45 / 46 / 54 / 65 / 76 / 147 / 575.
+// Past 32 rows the weights are read again for each 32.
 
 #include <type_traits>
 
@@ -195,7 +199,7 @@ template <int FMT, typename TS, int SG, int MT> struct BlockBf16 {
   // 8 % more on the down shape); 32 rows leave no registers for the activations
   // and scales (168 at three waves per SIMD), which are fetched when their stage
   // begins; so are more than 8 bytes of scales a tile (INT4, whose offset takes
-  // registers too: more than one scale).
+  // registers too: more than one scale; with four fp32 scales it spills two).
   static constexpr bool kAhead = MT == 1;
   static constexpr bool kScalesAhead = kAhead && (FMT == MOE_W4_INT4 ? SG == 1 : sizeof(Scales<TS, SG>) <= 8);
 
@@ -636,10 +640,11 @@ __global__ __launch_bounds__(kMaxWaves * MOE_WAVE, 3) void gemv_w4_kernel(GemvAr
 // How many waves share a column block: up to four while each keeps eight
 // stages (a wave's first loads and the sums' meeting cost about four stages'
 // time), and up to eight with four stages each where the blocks would not fill
-// the card's SIMDs once.  Measured with four rows an expert, in us, for 1 / 2 /
-// 4 / 8 waves: L 32, 4096 x 7168: 96 / 92 / 87 / 109; L 32, 7168 x 2048: 55 / 48 /
-// 56 / 91; L 64, 4096 x 1408: 36 / 40 / 46 / 92; L 1, 4096 x 7168: 52 / 28 / 18 / 14;
-// L 1, 7168 x 2048: 17 / 11 / 7.8 / 7.9.
+// the card's SIMDs once.  Measured with four rows an expert, INT4 with a scale per
+// 128, in us, for 1 / 2 / 4 / 8 waves, FP8 rows and bf16 rows: L 32, 4096 x 7168: 81 / 84 /
+// 82 / 102 and 79 / 80 / 77 / 92; L 32, 7168 x 2048: 54 / 46 / 54 / 85 and 53 / 43 / 43 / 65; L
+// 64, 4096 x 1408: 35 / 37 / 43 / 85 and 34 / 34 / 38 / 61; L 1, 4096 x 7168: 46 / 25 / 16 / 13
+// and 41 / 23 / 14 / 12; L 1, 7168 x 2048: 15 / 10 / 7.2 / 7.4 and 14 / 9.3 / 6.6 / 6.2.
 void pick_split(GemvArgs& p, int L) {
   const int KS = p.K / 128;
   const int64_t blocks = static_cast<int64_t>(L) * (p.N / 64);

@@ -15,8 +15,8 @@
 // -448, so groups whose amax is no finite number are looked at once more.
 //
 // Bound by memory.  Forward, 8192 x 7168 bf16 with residual to h and FP8 (413
-// MB): 69.4 us, 5.9 TB/s; backward, 16384 x 4096 bf16 with dh (537 MB): 89.0 us
-// and 4.2 for the reduction of d_w, 5.8 TB/s.
+// MB): 69.6 to 72 us, 5.9 TB/s; backward, 16384 x 4096 bf16 with dh (537 MB): 91.5
+// to 95 us and 4.2 for the reduction of d_w, 5.6 TB/s.
 
 #include "block_common.h"
 #include "router_common.h"
@@ -170,6 +170,12 @@ __global__ __launch_bounds__(kMaxWaves * 64) void add_rms_norm_kernel(const T* x
 // 1001 x 1408 fp32, 512 / 768 / 1024: 10 / 11 / 12.  Narrow rows have few waves
 // a block and get more blocks, with 32 rows each at least (65536 x 512 bf16,
 // 1024 / 2048 / 4096 blocks: 66 / 57 / 59; 32768 x 1408, 1024 / 2048: 68 / 82).
+// Wider and fp32 rows, reduction included, 256 / 512 / 1024 / 2048 blocks: bf16
+// 1024 x 7168 21.3 / 21.9 / 26.8 / 26.8; 2048 x 7168 34.7 / 32.4 / 37.9 / 46.8; 8192 x
+// 7168 110 / 88 / 91 / 102; 8192 x 5120 102 / 64 / 85 / 82 (there the rule's 1024 are
+// not the best); 2048 x 16384 56 / 65 / 84 / 110; fp32 1024 x 7168 31 / 36 / 41 / 41;
+// 8192 x 7168 194 / 198 / 206 / 220; 8192 x 4096 123 / 103 / 107 / 115; 16384 x 1408 121 /
+// 88 / 76 / 85.
 inline int bw_blocks(int T, int H) {
   const int waves = (H / 8 + 63) / 64;
   const int base = T >= 8192 ? 1024 : 512;
@@ -313,12 +319,17 @@ template <typename T, typename TW, int VPL, bool NT> void fw_launch(const FwArgs
 
 template <typename T, typename TW> void fw_pick(const FwArgs& a) {
   const bool nt = static_cast<int64_t>(a.T) * a.H * static_cast<int64_t>(sizeof(T)) >= kStreamBytes;
-  // Few rows: a row on as many waves as it has chunks for.  Many: up to four
+  // Below 32 MB: a row on as many waves as it has chunks for.  Past it: up to four
   // chunks a lane, so that a compute unit holds more rows at once (8192 x 7168
   // bf16 with residual to h and FP8, us: one chunk a lane 87, two 73.6, three
   // 73.3, four 71.1 = 5.8 TB/s, seven 75; two with plain loads and stores 79,
   // non-temporal loads only 79, stores only 76; codes stored past the
   // caches too 73.0).
+  // With y as well, us for one / two / four: bf16, below 128 x 7168 5.1 / 5.7 / 7.7, 1024
+  // x 7168 16.8 / 16.8 / 17.8, 2048 x 7168 29.0 / 30.4 / 33.0, 8192 x 1408 22.3 / 24.9 /
+  // 26.1, past 4096 x 4096 27.9 / 28.2 / 31.6, 8192 x 7168 92 / 85 / 88; fp32, below 512 x
+  // 7168 15.0 / 15.5 / 14.4, 1024 x 7168 26.3 / 27.4 / 27.5, past 4096 x 7168 96 / 103 /
+  // 100, 8192 x 4096 107 / 111 / 116 (there one would be 4 % faster than the rule).
   const int chunks = a.H / 8;
   if (!nt) {
     if (chunks <= 64 * kMaxWaves) fw_launch<T, TW, 1, false>(a);
@@ -347,6 +358,12 @@ template <typename T, typename TW, int VPL, bool NT> void bw_launch(const BwArgs
       static_cast<const TW*>(a.weight), a.eps, a.T, a.H, static_cast<T*>(a.dx), a.part);
 }
 
+// One chunk a lane up to 8 waves of bf16 and 16 of fp32 rows, then two.  With the
+// reduction, us for one / two: bf16 4096 x 4096 29.4 / 30.9, 16384 x 4096 95 / 97, 8192 x
+// 5120 80 / 85 (at the edge, where one would be faster), 1024 x 7168 23.1 / 21.9, 8192
+// x 7168 98 / 92, 8192 x 8192 106 / 102; fp32 16384 x 1408 76 / 78, 8192 x 4096 107 / 109,
+// 1024 x 7168 36 / 31, 8192 x 7168 206 / 187 (from about 7168 on two would be).  The
+// two-chunk bf16 form fills 128 VGPRs and spills two or three of them.
 template <typename T, typename TW> void bw_pick(const BwArgs& a) {
   const bool nt = static_cast<int64_t>(a.T) * a.H * static_cast<int64_t>(sizeof(T)) >= kStreamBytes;
   if (a.H <= 64 * 8 * (sizeof(T) == 4 ? 16 : 8)) nt ? bw_launch<T, TW, 1, true>(a) : bw_launch<T, TW, 1, false>(a);
