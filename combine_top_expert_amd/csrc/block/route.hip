@@ -474,7 +474,8 @@ __global__ __launch_bounds__(kThreads) void group_topk_kernel(RouteArgs a) {
   if (!BIAS && !near) {
     if (two_in_zone(my >= 0, x)) {
       const float o = __shfl_down(x, 1);
-      near = __ballot(lane < a.K && __shfl_down(my, 1) >= 0 && may_tie(x, o)) != 0;
+      const int next = __shfl_down(my, 1);              // by every lane: lane K - 1 reads lane K
+      near = __ballot(lane < a.K && next >= 0 && may_tie(x, o)) != 0;
     }
   }
   if (near) {
