@@ -312,11 +312,13 @@ __global__ __launch_bounds__(kThreads) void group_topk_kernel(RouteArgs a) {
 
   // Whether logits v > o may have the same fp64 score.  Neighbouring fp32 logits
   // have different ones, but for sigmoid from 23 on, where 1 + exp(-l) is rounded
-  // to steps of 2^-52 (from 37 on all are 1), where the score underflows (-708
-  // below the largest, with sigmoid below 0), and next to 0, where logits lie
-  // closer than fp64 can tell 1 + l (or l less the largest) apart.
+  // to steps of 2^-52 (from 37 on all are 1; fast_exp is off by 3e-15 at 20, less
+  // above), where the score underflows (-708 below the largest, with sigmoid below
+  // 0), and next to 0, where logits lie closer than fp64 can tell 1 + l (or l less
+  // the largest) apart.
   auto may_tie = [&](float v, float o) {
-    return v > o && (v - o < 1e-12f || (SIG ? o > 20.f || v < -700.f : v - m < -700.f));
+    const bool out = SIG ? (o > 20.f && fast_exp(-o) - fast_exp(-v) < 8e-15f) || v < -700.f : v - m < -700.f;
+    return v > o && (v - o < 1e-12f || out);
   };
   // whether it can hold at all: of two logits, both below 2^-15 (1e-12 apart
   // means that), or outside an ordinary range

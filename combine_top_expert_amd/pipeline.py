@@ -122,7 +122,8 @@ class MoELayer:
         byte), the scales [L,2I,H/group] and [L,H,I/group] (fp32 or bf16);
         both are packed (moe_pack_w4), and only the packed copies are kept.
         New weights of the same sizes and dtypes are packed over the old copies,
-        so bound and captured steps read them; with another scale group or
+        so bound and captured steps read them (on the current stream: steps on
+        others have to be over, or wait for it); with another scale group or
         scale dtype such steps have to be bound and captured again, as with
         every other weight type."""
         if self.shape.wdt in _W4:
