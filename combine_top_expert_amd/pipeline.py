@@ -114,7 +114,12 @@ class MoELayer:
         self.w13 = self.w13_scales = self.w2 = self.w2_scales = self.w13_packed = None
         self.w4 = None                                       # packed 4-bit weights: (codes, scales) of W13 and W2
         self.adamw = None                                    # the optimizer's state (prepare_step)
-        self.has_weight_grads = False                        # dw13 and dw2 hold a backward's gradients
+        self._forget_weight_grads()
+
+    def _forget_weight_grads(self):
+        self.has_weight_grads = False                        # dw13 and dw2 hold gradients that no step has applied
+        self._grads_made = False                             # some backward of these weights, run or captured, fills them
+        self._captured_grads = None                          # whether the last captured backward does (None: there is none)
 
     def set_fused(self, fused: bool):
         """Switch the gate/up GEMM between the fused SiLU*up epilogue (the
@@ -168,6 +173,7 @@ class MoELayer:
             self.w4 = held
             return
         self.w13, self.w2, self.w13_scales, self.w2_scales = w13, w2, w13_scales, w2_scales
+        self._forget_weight_grads()                          # they were of the weights before
         self.w13_packed = None
         if pack_w13:
             self.w13_packed = torch.empty_like(w13)
@@ -280,8 +286,7 @@ class MoELayer:
         w, lay = ((self.w13_packed, MOE_W_PACKED) if self.w13_packed is not None
                   else (self.w13, MOE_W_ROW_MAJOR))
         st = [
-            ("combine_bw", lambda: moe_combine_backward(dy, self.out, self.slot_of, topk_weights,
-                                                        self.d_out, self.d_w)),
+            ("combine_bw", lambda: self._combine_bw(dy, topk_weights)),
             ("gemm_dz", lambda: moe_grouped_gemm_w2(self.d_out, None, self.w2_t, None, self.counts,
                                                     self.offsets, self.dz, workspace=self.gemm_workspace)),
         ]
@@ -314,9 +319,24 @@ class MoELayer:
             ]
         return st
 
+    def _capturing(self):
+        with torch.cuda.device(self.buf.device):
+            return torch.cuda.is_current_stream_capturing()
+
+    def _combine_bw(self, dy, topk_weights):
+        moe_combine_backward(dy, self.out, self.slot_of, topk_weights, self.d_out, self.d_w)
+        if self._capturing():
+            self._captured_grads = False
+        else:
+            self.has_weight_grads = False
+
     def _wgrad_w13(self):
         moe_grouped_gemm_wgrad(self.dg, self.buf, self.counts, self.offsets, self.dw13)
-        self.has_weight_grads = True
+        self._grads_made = True
+        if self._capturing():                                # nothing has run yet
+            self._captured_grads = True
+        else:
+            self.has_weight_grads = True
 
     def backward(self, dy, topk_weights, weight_grads=True, fuse_silu=True):
         """Gradients of the last forward for dy [T,H]: returns (dx [T,H],
@@ -358,23 +378,35 @@ class MoELayer:
             for m, w in zip(self.adamw["masters"], self.adamw["weights"]):
                 m.copy_(w)
 
-    def step(self, lr, number=None, grad_scale=None):
+    def step(self, lr, number=None, grad_scale=None, reuse_grads=False):
         """One AdamW update of W13 and W2 (the tensors of set_weights), in place,
-        from the dw13 and dw2 of the last backward with weight_grads; the copies
-        that the forward and the backward read (packed and transposed weights)
-        are written again.  lr and number (of this update; counted here if not
-        given) are numbers, or device tensors (fp32, int64) that a captured
-        step reads anew; grad_scale: a device factor of the gradients (not
-        finite: the weights and moments stay, and the count goes on).  Nothing
-        waits."""
+        from the dw13 and dw2 of the last backward, which has to have made them
+        (weight_grads); the copies that the forward and the backward read
+        (packed and transposed weights) are written again.  lr and number (of
+        this update; counted here if not given) are numbers, or device tensors
+        (fp32, int64) that a captured step reads anew; grad_scale: a device
+        factor of the gradients (not finite: the weights and moments stay, and
+        the count goes on).  Nothing waits.
+
+        A backward's gradients are applied once.  reuse_grads takes dw13 and dw2
+        as they are: again, the last ones that a backward made, or those of a
+        captured backward that has been replayed (a captured step behind its
+        captured backward needs no such word)."""
         o = self.adamw
         if o is None or o["weights"][0] is not self.w13 or o["weights"][1] is not self.w2:
             raise ValueError("step needs prepare_step after set_weights")
-        if not self.has_weight_grads:
-            raise ValueError("step needs a backward with weight_grads")
+        capturing = self._capturing()
+        fresh = self.has_weight_grads
+        if capturing:
+            fresh = self._grads_made if self._captured_grads is None else self._captured_grads
+        if not (fresh or reuse_grads and self._grads_made):
+            raise ValueError("step needs a backward with weight_grads whose gradients it has not applied yet "
+                             "(reuse_grads takes those of a replayed graph, or the same again)")
         moe_adamw_step(o["weights"], [self.dw13, self.dw2], *o["moments"], lr, o["number"] + 1 if number is None else number,
                        masters=o["masters"], exp_avg_scales=o["scales"][0], exp_avg_sq_scales=o["scales"][1],
                        grad_scale=grad_scale, **o["hyper"])
+        if not capturing:
+            self.has_weight_grads = False
         if number is None:
             o["number"] += 1
         elif not isinstance(number, torch.Tensor):
