@@ -53,7 +53,8 @@ template <bool S8, bool MASTER> struct Batch {
 
 struct Config {
   float b1, a1, b2, a2, eps;                       // a1 = 1 - b1, a2 = 1 - b2
-  float rate, decay, root2;                        // lr / (1 - b1^t), lr wd, 1 / sqrt(1 - b2^t)
+  float rate, decay, root2;                        // unit lr / (1 - b1^t), lr wd, unit / sqrt(1 - b2^t)
+  float unit;                                      // of the quotient's denominator (eps times it, too): a power of two
   double lr, wd, d1, d2, inv1;                     // for numbers on the device: b1, b2, 1 / (1 - b1^t)
   uint32_t seed, step;                             // step's low 32 bits
   const float* lr_device;
@@ -273,9 +274,9 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Batch<S8, MASTER>
       const double inv1 = c.step_device ? 1.0 / (1.0 - power(c.d1, t)) : c.inv1;
       const double p2 = c.step_device ? power(c.d2, t) : 0.0;
       if (threadIdx.x == 0) {
-        shared[0] = static_cast<float>(lr * inv1);
+        shared[0] = static_cast<float>(lr * inv1) * c.unit;
         shared[1] = static_cast<float>(lr * c.wd);
-        shared[2] = c.step_device ? static_cast<float>(1.0 / sqrt(1.0 - p2)) : c.root2;
+        shared[2] = c.step_device ? static_cast<float>(1.0 / sqrt(1.0 - p2)) * c.unit : c.root2;
       }
     }
     __syncthreads();
@@ -296,7 +297,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Batch<S8, MASTER>
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
 // each operation of the states rounds once: one that is rounded to 8 bits next to a border is then the same
-// for everyone who computes it in fp32.  The update's quotient takes the hardware's reciprocal (1 ulp).
+// for everyone who computes it in fp32.  The update's quotient takes the hardware's reciprocal (1 ulp), of a
+// denominator that the unit keeps in its range.
 #pragma clang fp contract(off)
       const float gk = g[u][k] * gs;
       m[u][k] = c.b1 * m[u][k] + c.a1 * gk;
@@ -409,7 +411,12 @@ extern "C" moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int count,
               MOE_ERR_INVALID_ARG);
   }
   Config c{};
-  c.lr = f.lr, c.wd = f.weight_decay, c.eps = static_cast<float>(f.eps);
+  // The denominator, at least eps and at most 2^64 / sqrt(2^-53) + eps, in a unit that makes it a normal number with a
+  // normal reciprocal also where eps itself is not one; 1 for any usual eps.
+  c.unit = f.eps < 0x1p-100 ? 0x1p32f : f.eps > 0x1p100 ? 0x1p-32f : 1.f;
+  c.eps = static_cast<float>(f.eps * c.unit);
+  if (f.eps > 0.0 && c.eps < 0x1p-117f) c.eps = 0x1p-117f;           // 2^-149 in the unit: fp32's least number
+  c.lr = f.lr, c.wd = f.weight_decay;
   c.b1 = static_cast<float>(f.beta1), c.a1 = static_cast<float>(1.0 - f.beta1);
   c.b2 = static_cast<float>(f.beta2), c.a2 = static_cast<float>(1.0 - f.beta2);
   c.d1 = f.beta1, c.d2 = f.beta2;
@@ -418,8 +425,8 @@ extern "C" moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int count,
   if (!f.step_device) {
     c.step = static_cast<uint32_t>(f.step);
     c.inv1 = 1.0 / (1.0 - pow(f.beta1, static_cast<double>(f.step)));
-    c.root2 = static_cast<float>(1.0 / sqrt(1.0 - pow(f.beta2, static_cast<double>(f.step))));
-    c.rate = static_cast<float>(f.lr * c.inv1);
+    c.root2 = static_cast<float>(1.0 / sqrt(1.0 - pow(f.beta2, static_cast<double>(f.step)))) * c.unit;
+    c.rate = static_cast<float>(f.lr * c.inv1) * c.unit;
     c.decay = static_cast<float>(f.lr * f.weight_decay);
   }
   if (p_dt == MOE_F32)

@@ -135,7 +135,8 @@ typedef struct moe_adamw_config {
  *   g = grad * grad_scale
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
  *   p = p - lr weight_decay p - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
- * with p = master, of which param is then the rounded copy, or p = param.
+ * with p = master, of which param is then the rounded copy, or p = param.  An eps
+ * above 0 counts as 2^-149, fp32's least number, at least.
  *   s_dt F32: m and v are fp32.
  *   s_dt FP8_E4M3: m and sqrt(v) are e4m3fn codes with one fp32 scale per 128
  *   neighbouring elements (value = code * scale, scale = max * fp32(1/448)
