@@ -386,7 +386,9 @@ class MoELayer:
         this update; counted here if not given) are numbers, or device tensors
         (fp32, int64) that a captured step reads anew; grad_scale: a device
         factor of the gradients (not finite: the weights and moments stay, and
-        the count goes on).  Nothing waits.
+        the count goes on).  Nothing waits.  After a device number the count is
+        the caller's, until a step is given a number from the host; a captured
+        step has to be given one either way.
 
         A backward's gradients are applied once.  reuse_grads takes dw13 and dw2
         as they are: again, the last ones that a backward made, or those of a
@@ -402,6 +404,10 @@ class MoELayer:
         if not (fresh or reuse_grads and self._grads_made):
             raise ValueError("step needs a backward with weight_grads whose gradients it has not applied yet "
                              "(reuse_grads takes those of a replayed graph, or the same again)")
+        if number is None and o["number"] is None:
+            raise ValueError("step needs the update's number: those before it were on the device")
+        if number is None and capturing:
+            raise ValueError("a captured step needs number: its replays would all be the update that is counted now")
         moe_adamw_step(o["weights"], [self.dw13, self.dw2], *o["moments"], lr, o["number"] + 1 if number is None else number,
                        masters=o["masters"], exp_avg_scales=o["scales"][0], exp_avg_sq_scales=o["scales"][1],
                        grad_scale=grad_scale, **o["hyper"])
@@ -409,8 +415,8 @@ class MoELayer:
             self.has_weight_grads = False
         if number is None:
             o["number"] += 1
-        elif not isinstance(number, torch.Tensor):
-            o["number"] = number
+        else:
+            o["number"] = None if isinstance(number, torch.Tensor) else number
         if self.w13_packed is not None:
             moe_pack_w13(self.w13, self.w13_packed)
         self.refresh_transposed_weights()
