@@ -160,16 +160,20 @@ class MoELayer:
                 pairs = [self._to_mx4(w) for w in (w13, w2)]
             elif w13_scales is None or w2_scales is None:
                 raise ValueError("w13_scales and w2_scales are required for 4-bit weights")
-            held, pack = [], []
-            for i, (codes, scales) in enumerate(pairs):
-                old = self.w4[i] if self.w4 is not None else (None, None)
-                packed = tuple(o if o is not None and (o.shape, o.dtype, o.device) == (t.shape, t.dtype, t.device)
-                               else torch.empty_like(t) for o, t in zip(old, (codes, scales)))
-                pack.append(moe_pack_mx4(codes, scales, *packed, bind=True) if wdt == "mx4"
-                            else moe_pack_w4(codes, scales, _W4[wdt], *packed, bind=True))
-                held.append(packed)
-            for f in pack:                                   # both were checked before either is written
-                f()
+            same = lambda o, t: o is not None and (o.shape, o.dtype, o.device) == (t.shape, t.dtype, t.device)  # noqa: E731
+            old = self.w4 or [(None, None)] * 2
+            held = [tuple(o if same(o, t) else torch.empty_like(t) for o, t in zip(*p)) for p in zip(old, pairs)]
+            # Sizes and addresses are refused before anything is written.  Copies that steps may read are
+            # written once neither is: W2 goes beside the old one until W13 has been taken.
+            w2_new = tuple(torch.empty_like(h) if h is o else h for h, o in zip(held[1], old[1]))
+            for (codes, scales), packed in ((pairs[1], w2_new), (pairs[0], held[0])):
+                if wdt == "mx4":
+                    moe_pack_mx4(codes, scales, *packed)
+                else:
+                    moe_pack_w4(codes, scales, _W4[wdt], *packed)
+            for h, n in zip(held[1], w2_new):
+                if h is not n:
+                    h.copy_(n)
             self.w4 = held
             return
         self.w13, self.w2, self.w13_scales, self.w2_scales = w13, w2, w13_scales, w2_scales
