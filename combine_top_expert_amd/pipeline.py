@@ -176,12 +176,11 @@ class MoELayer:
                     h.copy_(n)
             self.w4 = held
             return
-        self.w13, self.w2, self.w13_scales, self.w2_scales = w13, w2, w13_scales, w2_scales
-        self._forget_weight_grads()                          # they were of the weights before
-        self.w13_packed = None
+        packed = torch.empty_like(w13) if pack_w13 else None
         if pack_w13:
-            self.w13_packed = torch.empty_like(w13)
-            moe_pack_w13(w13, self.w13_packed)
+            moe_pack_w13(w13, packed)                        # refused: the layer stays as it was
+        self.w13, self.w2, self.w13_scales, self.w2_scales, self.w13_packed = w13, w2, w13_scales, w2_scales, packed
+        self._forget_weight_grads()                          # they were of the weights before
 
     @staticmethod
     def _to_mx4(w):
