@@ -46,8 +46,8 @@ int moe_experts_abi_version(void);
  * leaves as NaN, not as numbers.
  *   x [rows,K] x_dt in {F32, BF16}; codes [rows,K/2], scales [rows,K/32]
  *   values [rows,K] x_dt, or NULL: what the codes stand for (exact; infinite
- *   where that is 2^128, of numbers above 3.75 * 2^126), for a training pass that
- *   sees the quantised rows; may be x itself
+ *   where that is 2^128 or more, of numbers from 3.5 * 2^126 on), for a training
+ *   pass that sees the quantised rows; may be x itself
  * Limits: K % 32 == 0, rows * K <= 2^40; x, codes and values 16-byte aligned.
  */
 moe_status moe_quantize_mx4(const void* x, moe_dtype x_dt, int64_t rows, int K, void* codes, void* scales,
@@ -158,8 +158,8 @@ typedef struct moe_adamw_config {
  *   tensors[count] is host memory and read before the call returns; p_dt, g_dt
  *   in {F32, BF16}; master only with p_dt BF16, for all tensors or for none.
  * Limits: lr, eps and weight_decay finite and >= 0, beta1 and beta2 in [0, 1), step >= 1
- * (without step_device); 0 <= n <= 2^40; all device pointers 16-byte aligned (lr_device
- * and grad_scale 4, step_device 8).  Tensors of one call may not overlap.
+ * (without step_device); 0 <= n <= 2^40; all device pointers 16-byte aligned (the
+ * states' scales, lr_device and grad_scale 4, step_device 8).  Tensors of one call may not overlap.
  */
 moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int count, moe_dtype p_dt, moe_dtype g_dt,
                           moe_dtype s_dt, const moe_adamw_config* config, hipStream_t stream);
