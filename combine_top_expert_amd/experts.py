@@ -196,6 +196,15 @@ def _list(name, tensors, sizes, device, dtypes, written=True):
     return pointers
 
 
+def _distinct(lists, sizes):
+    """Refuse a tensor that two of these lists of pointers name (each names it once at most)."""
+    if 0 in sizes:
+        lists = [[v for v, n in zip(pointers, sizes) if n] for pointers in lists]
+    used = [pointers for pointers in lists if any(pointers)]
+    if len(set().union(*used)) < sum(map(len, used)):
+        raise ValueError("params, masters, exp_avgs, exp_avg_sqs and their scales name the same tensor twice")
+
+
 def _scalar(name, t, dtype, device):
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -251,13 +260,15 @@ def moe_adamw_step(params, grads, exp_avgs, exp_avg_sqs, lr, step, betas=(0.9, 0
     if not s8 and (exp_avg_scales is not None or exp_avg_sq_scales is not None):
         raise ValueError("exp_avg_scales and exp_avg_sq_scales go with 8-bit states only")
     zeros = [0] * len(sizes)
-    table = (AdamwTensor * len(sizes))(*zip(
+    lists = (
         _list("params", params, sizes, device, _REAL),
         zeros if masters is None else _list("masters", masters, sizes, device, _F32),
         _list("grads", grads, sizes, device, _REAL, written=False),
         _list("exp_avgs", exp_avgs, sizes, device, state), _list("exp_avg_sqs", exp_avg_sqs, sizes, device, state),
         _list("exp_avg_scales", exp_avg_scales, blocks, device, _F32) if s8 else zeros,
-        _list("exp_avg_sq_scales", exp_avg_sq_scales, blocks, device, _F32) if s8 else zeros, sizes))
+        _list("exp_avg_sq_scales", exp_avg_sq_scales, blocks, device, _F32) if s8 else zeros, sizes)
+    _distinct(lists[:2] + lists[3:7], sizes)
+    table = (AdamwTensor * len(sizes))(*zip(*lists))
     if not 0 <= seed < 1 << 32:
         raise ValueError(f"seed is {seed}, expected 32 bits")
     config = AdamwConfig(beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay, seed=seed)
