@@ -14,8 +14,8 @@ from pathlib import Path
 
 import torch
 
-from . import MOE_BF16, MOE_EPI_SILU_MUL, MOE_EPI_STORE_G, MOE_F32, MOE_FP8_E4M3, MoEError, _need, _offsets
-from .block import (_CODE, _F32, _FP8, _I32, _INT_MAX, _REAL, _U8, _current_device, _pointers, _raw_stream, _refuse,
+from . import MOE_EPI_SILU_MUL, MOE_EPI_STORE_G, MOE_F32, MOE_FP8_E4M3, MoEError, _need, _offsets
+from .block import (_CODE, _F32, _FP8, _I32, _INT_MAX, _REAL, _U8, _current_device, _pointers, _raw_stream,
                     _too_large)
 
 __all__ = [
