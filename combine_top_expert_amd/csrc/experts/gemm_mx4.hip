@@ -24,9 +24,11 @@
 //
 // Bound by the loads that a CU's memory path holds at a time, about 100 of 128
 // bytes (counters at 4 / 128 rows an expert: 104 / 85 in flight, 1315 / 770 cycles
-// each): with few rows that is the weights' stream at 6.2 to 6.6 TB/s; with more,
-// the rows' reads from L2 take places in it, and at 512 rows the matrix cores come to
-// 56 % of what they reach on random codes (6.5 PFLOP/s; 8.5 on constant ones).
+// each): with few rows that is the weights' stream, at 6.2 to 6.6 TB/s in gate/up and 5.1
+// in the shorter down product; with more, the reads of rows and of their scales from L2
+// take places in it.  The scales take as many as the rows do, a quarter of all at 128
+// rows, as each thread opens a line of its own for 16 bytes.  At 512 rows the matrix cores
+// come to 56 % of what they reach on random codes (6.5 PFLOP/s; 8.5 on constant ones).
 // Measured, us, 32 experts with the same number of rows, 4 / 16 / 32 / 64 / 128 / 256 / 512:
 // gate/up 4096 x 7168 (500 MB) 77 / 79 / 81 / 90 / 109 / 153 / 268 (3.6 PFLOP/s); down 7168 x
 // 2048 (250 MB) 49 / 51 / 54 / 60 / 75 / 111 / 190.  One decode step (128 tokens, about 70 rows,

@@ -8,7 +8,7 @@
 //
 // Bound by memory: the bytes of x, and 17/32 of a byte a value back.  470 M bf16
 // values (1.19 GB) take 191 us, 6.2 TB/s; dispatch of 8192 tokens of 7168 bf16 columns to 32 of 256 experts
-// (3300 of them have one: 63 MB, which the 256 MB cache holds) 13.2 us, of 128 tokens 2.3 us, a launch.
+// (3300 of them have one: 63 MB, which the 256 MB cache holds) 12.2 to 13.5 us, of 128 tokens 2.8 us, a launch.
 
 #include "experts_common.h"
 
