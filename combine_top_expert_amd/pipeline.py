@@ -414,8 +414,7 @@ class MoELayer:
         moe_adamw_step(o["weights"], [self.dw13, self.dw2], *o["moments"], lr, o["number"] + 1 if number is None else number,
                        masters=o["masters"], exp_avg_scales=o["scales"][0], exp_avg_sq_scales=o["scales"][1],
                        grad_scale=grad_scale, **o["hyper"])
-        if not capturing:
-            self.has_weight_grads = False
+        self.has_weight_grads = False                        # applied, or a graph's to apply
         if number is None:
             o["number"] += 1
         else:

@@ -174,3 +174,22 @@ def test_captured_step(ep):
         refused.backward(weight_grads=False)
         with pytest.raises(ValueError, match="weight_grads"):
             refused.layer.step(lr, number=number)
+
+
+def test_eager_step_after_a_captured_one(ep):
+    """What a captured step applies is no eager step's: neither the gradients of its replays nor those before them."""
+    announce("eager step after a captured one")
+    c = Case()
+    c.backward()
+    number = torch.ones(1, dtype=torch.int64, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with captured(graph):
+        c.backward()
+        c.layer.step(1e-2, number=number)
+    c.refused(number=1)
+    graph.replay()
+    torch.cuda.synchronize()
+    c.refused(number=2)
+    c.backward()
+    c.layer.step(1e-2, number=2)
+    assert c.layer.adamw["number"] == 2
